@@ -64,7 +64,7 @@ enum {
                             Methodology section 3: clipping heuristics)       */
 };
 
-enum { ADMMQ_DTYPE_F32 = 0, ADMMQ_DTYPE_BF16 = 1 };
+enum { ADMMQ_DTYPE_F32 = 0, ADMMQ_DTYPE_BF16 = 1, ADMMQ_DTYPE_F16 = 2 };
 
 /* Split precision of the eigenbasis GEMMs (fp32-accurate products on tf32 /
  * bf16 tensor cores; see "operand encoding" below). */
@@ -250,6 +250,78 @@ int admmq_solve(admmq_ctx* ctx, uint8_t* codes_dev, float* scale_dev, float* zer
  * section 3; the pages do not define the bit layout.) */
 int admmq_pack(const uint8_t* codes_dev, int d_in, int d_out, int bits, uint32_t* packed_dev,
                void* stream);
+
+/* Product of activations with packed codes (admmq_pack), the linear layer
+ * that a solve or GPTQ returned:
+ *   out[i][j] = sum over groups G of scale[j][G] sum_{k in G} (code[j][k] - zero[j][G]) x[i][k]
+ * (scale (code - zero) is the weight, as everywhere in this library).  The
+ * differences code - zero are exact and every group's sum is formed in fp32
+ * before its scale is applied; nothing is rounded to 16 bits but the output.
+ *   x_dev      bf16 or fp16 (x_dtype) [m][d_in], rows ldx elements apart
+ *              (ldx >= d_in, a multiple of 8), 16-byte aligned.
+ *   packed_dev uint32 [d_out][d_in * bits / 32], 16-byte aligned.
+ *   scale_dev, zero_dev fp32 [d_out][d_in / group]; zero points are integers
+ *              in [0, 2^bits - 1] (as the solve, the RTN start and GPTQ give them).
+ *   out_dev    fp32, bf16 or fp16 (out_dtype) [m][d_out], contiguous, 16-byte
+ *              aligned.
+ * m >= 0 (nothing is launched for 0), at most 2^30.  Deterministic: no sum's
+ * order depends on timing. */
+int admmq_packed_matmul(const void* x_dev, int x_dtype, int64_t m, int64_t ldx,
+                        const uint32_t* packed_dev, const float* scale_dev, const float* zero_dev,
+                        int d_in, int d_out, int bits, int group, void* out_dev, int out_dtype,
+                        void* stream);
+
+/* ------------------------------------------- microscaled 4-bit floating point --
+ * Matrices of e2m1 elements (0, 1/2, 1, 3/2, 2, 3, 4, 6 and their negatives)
+ * with one 8-bit scale per block of a row, the tensor cores' own formats:
+ *   ADMMQ_MX_MXFP4  blocks of 32, scale byte e8m0: step t = 2^(byte - 127),
+ *                   255 = NaN;
+ *   ADMMQ_MX_NVFP4  blocks of 16, scale byte e4m3 (0x7F = NaN) on top of one
+ *                   fp32 scale g of the whole matrix: t = fl32(e4m3(byte) g).
+ * value = element x t.  (Calibrated weights use the integer grids above; these
+ * formats need no calibration and their products run on the 4-bit tensor
+ * cores.)
+ *   codes  u8 [rows][k / 2]: element 2i of a row in the low nibble of byte i.
+ *   scale  u8, tiles of 128 rows x 4 blocks (512 bytes), [ceil(rows / 128)]
+ *          [ceil(k / (4 block))][32][4][4]: row r, block c of a tile at byte
+ *          16 (r % 32) + 4 (r / 32) + c; bytes without a block are 0.
+ *   tensor_scale_dev  fp32 [1] on the device, positive and finite (0, the
+ *          scale of a matrix of zeros, reads and quantises as zeros); NULL
+ *          means 1.  Must be NULL for mxfp4.
+ * k is a multiple of 32, at most 2^24; rows >= 0 (nothing is launched for 0),
+ * at most 2^30.  codes, scale and the 16/32-bit matrices are 16-byte aligned,
+ * their row distances (ld, in elements) multiples of 16 bytes. */
+enum { ADMMQ_MX_MXFP4 = 0, ADMMQ_MX_NVFP4 = 1 };
+
+/* Bytes of the scale tiles of a [rows][k] matrix (0 for invalid sizes or no rows). */
+size_t admmq_mx_scale_bytes(int64_t rows, int k, int fmt);
+
+/* Quantise x [rows][k] (fp32, bf16 or fp16 per x_dtype, rows ld apart):
+ *   mxfp4: t = 2^(floor(log2 amax) - 2), at least 2^-127 (amax: the block's
+ *          largest magnitude; a block of zeros takes byte 0);
+ *   nvfp4: byte = e4m3(amax / (6 g)), nearest, ties to even, at most 448;
+ *   every element to the nearest multiple of t on the e2m1 grid, ties to the
+ *   even code, beyond 6 t to 6 t; a block with t = 0 to zeros.
+ * All decisions are those of exact arithmetic on the inputs.  A block that
+ * holds an infinity or NaN gets the NaN scale byte and zero codes: it reads as
+ * NaN.  codes_dev and scale_dev are written in full. */
+int admmq_mx_quantize(const void* x_dev, int x_dtype, int64_t rows, int k, int64_t ld, int fmt,
+                      const float* tensor_scale_dev, uint8_t* codes_dev, uint8_t* scale_dev,
+                      void* stream);
+
+/* out[r][c] = element x t (one fp32 multiplication), rounded once to out_dtype. */
+int admmq_mx_dequantize(const uint8_t* codes_dev, const uint8_t* scale_dev, int64_t rows, int k,
+                        int fmt, const float* tensor_scale_dev, void* out_dev, int out_dtype,
+                        int64_t ld, void* stream);
+
+/* out[i][j] = g_a g_b sum_k a[i][k] b[j][k]: the product of two matrices of one
+ * format, a [m][k] and b [n][k] (nn.Linear: activations and weights), sums in
+ * fp32, out [m][n] contiguous in out_dtype (fp32, bf16, fp16).  A NaN block
+ * makes the outputs of its row (of a) or column (of b) NaN.  Deterministic. */
+int admmq_mx_matmul(const uint8_t* a_codes_dev, const uint8_t* a_scale_dev,
+                    const float* a_tensor_scale_dev, const uint8_t* b_codes_dev,
+                    const uint8_t* b_scale_dev, const float* b_tensor_scale_dev, int64_t m, int n,
+                    int k, int fmt, void* out_dev, int out_dtype, void* stream);
 
 /* ------------------------------------------------------------ inspection --
  * Device buffers inside the workspace, for tests and diagnostics.

@@ -9,8 +9,10 @@ its Python binding) never calls it: there is no CPU fallback.
                    the bit-exact specification of the projection kernels
   spread           the oracle's own spread under W-update noise, which sets
                    the bar for free-running GPU solves
+  mx               microscaled 4-bit formats (rounding by brute force) and the
+                   weights behind packed codes, float64
 
 Pinned by tests/test_oracle_pins.py; "parity unpinned" parts are listed in the
 admmq_oracle module docstring.
 """
-from . import admmq_oracle, projection_fp32, spread  # noqa: F401
+from . import admmq_oracle, mx, projection_fp32, spread  # noqa: F401

@@ -20,10 +20,13 @@ GRID_MINMAX, GRID_LSQ, GRID_FROZEN, GRID_MSE = 0, 1, 2, 3
 GRID_MODES = {"minmax": GRID_MINMAX, "lsq": GRID_LSQ, "frozen": GRID_FROZEN, "mse": GRID_MSE}
 SPLIT_MODES = {"auto": 0, "3xtf32": 1, "mixed": 2, "f16": 3}
 SCHEDULES = {"fused": 0, "per_gemm": 1}
-DTYPE_F32, DTYPE_BF16 = 0, 1
+DTYPE_F32, DTYPE_BF16, DTYPE_F16 = 0, 1, 2
+DTYPES = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_F16}
+MX_FORMATS = {"mxfp4": 0, "nvfp4": 1}
+MX_BLOCK = {"mxfp4": 32, "nvfp4": 16}
 BUFFERS = ["sigma", "rsig", "hdiag", "lambda", "V", "C0", "P_hi", "P_lo", "T_hi", "T_lo",
            "E_hi", "E_lo", "Ht", "status", "row_in", "row_out"]
-ERR_TIMEOUT, ERR_RANGE = -6, -9
+ERR_INVALID_ARG, ERR_TIMEOUT, ERR_RANGE = -1, -6, -9
 
 
 class AdmmqError(RuntimeError):
@@ -123,6 +126,12 @@ def lib():
         "admmq_gptq_workspace_bytes": (_sz, [_i, _i, _i]),
         "admmq_gptq": (_i, [_vp, _vp, _i, _i, _i, _i, _i, ctypes.c_float, _i, _vp, _vp, _vp, _vp,
                             _sz, _vp]),
+        "admmq_packed_matmul": (_i, [_vp, _i, _i64, _i64, _vp, _vp, _vp, _i, _i, _i, _i, _vp, _i,
+                                     _vp]),
+        "admmq_mx_scale_bytes": (_sz, [_i64, _i, _i]),
+        "admmq_mx_quantize": (_i, [_vp, _i, _i64, _i, _i64, _i, _vp, _vp, _vp, _vp]),
+        "admmq_mx_dequantize": (_i, [_vp, _vp, _i64, _i, _i, _vp, _vp, _i, _i64, _vp]),
+        "admmq_mx_matmul": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _i64, _i, _i, _i, _vp, _i, _vp]),
     }
     for name, (res, args) in sig.items():
         if name.startswith("admmq_debug_") and not hasattr(L, name):
@@ -333,6 +342,176 @@ def pack(codes: torch.Tensor, bits: int, out: torch.Tensor | None = None, stream
         out = torch.empty((m, d * bits // 32), dtype=torch.int32, device=codes.device)
     _check(lib().admmq_pack(_ptr(codes), d, m, bits, _ptr(out), _stream(stream)), "admmq_pack")
     return out
+
+
+def _require(ok: bool, what: str):
+    if not ok:
+        raise AdmmqError(ERR_INVALID_ARG, what)
+
+
+def _is_matrix(x: torch.Tensor, dtypes) -> bool:
+    """A matrix on the GPU with unit column stride (rows may lie apart)."""
+    return x.is_cuda and x.dim() == 2 and x.dtype in dtypes and (x.stride(1) == 1 or x.shape[1] == 1)
+
+
+def _row_stride(x: torch.Tensor) -> int:
+    return x.stride(0) if x.shape[0] > 1 else x.shape[1]
+
+
+def _launch(name: str, device: torch.device, stream, *args):
+    """Call entry point `name` with `device` current, on `stream` (None: the
+    device's current stream)."""
+    if device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            return _launch(name, device, stream, *args)
+    s = stream if stream is not None else torch.cuda.current_stream()
+    rc = getattr(lib(), name)(*args, s.cuda_stream)
+    if rc != OK:
+        raise AdmmqError(rc, name)
+
+
+def _empty(shape, dtype, device, stream):
+    """A new tensor that belongs to the stream its kernel runs on."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _output(out, shape, dtype, x: torch.Tensor, stream, where: str):
+    """`out` after a check of its shape, type, device and layout, or a new tensor."""
+    if out is None:
+        return _empty(shape, dtype, x.device, stream)
+    _require(out.shape == shape and out.dtype == dtype and out.device == x.device
+             and out.is_contiguous(), f"{where}: out")
+    return out
+
+
+def packed_matmul(x: torch.Tensor, packed: torch.Tensor, scale: torch.Tensor, zero: torch.Tensor,
+                  bits: int, dtype: torch.dtype | None = None, out: torch.Tensor | None = None,
+                  stream=None) -> torch.Tensor:
+    """x [m][d_in] (bf16 or fp16) times the layer whose codes `pack` packed:
+    sum over groups of scale * (code - zero) . x, [m][d_out] in `dtype`
+    (x's by default).  The group size is d_in / scale.shape[1]."""
+    _require(_is_matrix(x, (torch.bfloat16, torch.float16)), "packed_matmul: x")
+    m, d = x.shape
+    _require(packed.dim() == 2 and packed.dtype == torch.int32 and packed.is_contiguous()
+             and packed.shape[1] * 32 == d * bits and packed.device == x.device,
+             "packed_matmul: packed")
+    n = packed.shape[0]
+    for name, t in (("scale", scale), ("zero", zero)):
+        _require(t.dtype == torch.float32 and t.dim() == 2 and t.shape[0] == n
+                 and t.is_contiguous() and t.device == x.device, f"packed_matmul: {name}")
+    groups = scale.shape[1]
+    _require(zero.shape[1] == groups and groups > 0 and d % groups == 0, "packed_matmul: groups")
+    dtype = dtype or x.dtype
+    _require(dtype in DTYPES, "packed_matmul: dtype")
+    out = _output(out, (m, n), dtype, x, stream, "packed_matmul")
+    _launch("admmq_packed_matmul", x.device, stream, x.data_ptr(), DTYPES[x.dtype], m,
+            _row_stride(x), packed.data_ptr(), scale.data_ptr(), zero.data_ptr(), d, n, bits,
+            d // groups, out.data_ptr(), DTYPES[dtype])
+    return out
+
+
+# ------------------------------------------- microscaled 4-bit floating point
+
+
+@dataclass(frozen=True)
+class MxTensor:
+    """A matrix [rows][k] of 4-bit elements with a scale per block of a row
+    (layouts in include/admmq.h): `codes` u8 [rows][k / 2], `scale` u8 in tiles
+    of 128 rows x 4 blocks, `fmt` "mxfp4" or "nvfp4", `tensor_scale` fp32 [1]
+    on the device (nvfp4; None means 1)."""
+    codes: torch.Tensor
+    scale: torch.Tensor
+    fmt: str = "mxfp4"
+    tensor_scale: torch.Tensor | None = None
+
+    def __post_init__(self):
+        c, s, g = self.codes, self.scale, self.tensor_scale
+        _require(self.fmt in MX_FORMATS, "MxTensor: fmt")
+        _require(c.is_cuda and c.dtype == torch.uint8 and c.dim() == 2 and c.is_contiguous()
+                 and c.shape[1] > 0 and c.shape[1] % 16 == 0, "MxTensor: codes")
+        _require(s.dtype == torch.uint8 and s.device == c.device and s.is_contiguous()
+                 and s.numel() == _mx_scale_numel(self.rows, self.k, self.fmt), "MxTensor: scale")
+        _check_tensor_scale(g, self.fmt, c.device, "MxTensor")
+
+    @property
+    def rows(self) -> int:
+        return self.codes.shape[0]
+
+    @property
+    def k(self) -> int:
+        return 2 * self.codes.shape[1]
+
+    @property
+    def device(self) -> torch.device:
+        return self.codes.device
+
+    def _ptrs(self):
+        g = self.tensor_scale
+        return self.codes.data_ptr(), self.scale.data_ptr(), None if g is None else g.data_ptr()
+
+
+def _mx_scale_numel(rows: int, k: int, fmt: str) -> int:
+    return -(-rows // 128) * -(-k // (4 * MX_BLOCK[fmt])) * 512
+
+
+def _check_tensor_scale(g, fmt: str, device, where: str):
+    if g is not None:
+        _require(fmt == "nvfp4" and g.dtype == torch.float32 and g.numel() == 1
+                 and g.device == device, f"{where}: tensor_scale")
+
+
+def mx_quantize(x: torch.Tensor, fmt: str = "mxfp4", tensor_scale: torch.Tensor | None = None,
+                stream=None) -> MxTensor:
+    """Round x [rows][k] (fp32, bf16 or fp16; k a multiple of 32) to a
+    microscaled 4-bit format: "mxfp4" (blocks of 32, power-of-two scales) or
+    "nvfp4" (blocks of 16, e4m3 scales on top of `tensor_scale`, usually
+    amax(x) / (448 * 6), fp32 [1] on the device)."""
+    _require(_is_matrix(x, DTYPES), "mx_quantize: x")
+    _require(fmt in MX_FORMATS, "mx_quantize: fmt")
+    _check_tensor_scale(tensor_scale, fmt, x.device, "mx_quantize")
+    rows, k = x.shape
+    _require(k > 0 and k % 32 == 0, "mx_quantize: k is a positive multiple of 32")
+    codes = _empty((rows, k // 2), torch.uint8, x.device, stream)
+    scale = _empty(_mx_scale_numel(rows, k, fmt), torch.uint8, x.device, stream)
+    _launch("admmq_mx_quantize", x.device, stream, x.data_ptr(), DTYPES[x.dtype], rows, k,
+            _row_stride(x), MX_FORMATS[fmt], None if tensor_scale is None else tensor_scale.data_ptr(),
+            codes.data_ptr(), scale.data_ptr())
+    return MxTensor(codes, scale, fmt, tensor_scale)
+
+
+def mx_dequantize(q: MxTensor, dtype: torch.dtype = torch.bfloat16,
+                  out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """The values of q, [rows][k] in `dtype` (fp32, bf16 or fp16)."""
+    _require(dtype in DTYPES, "mx_dequantize: dtype")
+    out = _output(out, (q.rows, q.k), dtype, q.codes, stream, "mx_dequantize")
+    codes, scale, g = q._ptrs()
+    _launch("admmq_mx_dequantize", q.device, stream, codes, scale, q.rows, q.k,
+            MX_FORMATS[q.fmt], g, out.data_ptr(), DTYPES[dtype], q.k)
+    return out
+
+
+def mx_matmul(a: MxTensor, b: MxTensor, dtype: torch.dtype = torch.bfloat16,
+              out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """a [m][k] times b [n][k] transposed (activations and nn.Linear weights,
+    both in one microscaled format), [m][n] in `dtype` (fp32, bf16 or fp16)."""
+    _require(a.fmt == b.fmt and a.k == b.k and a.device == b.device, "mx_matmul: a and b differ")
+    _require(b.rows > 0 and dtype in DTYPES, "mx_matmul: b or dtype")
+    out = _output(out, (a.rows, b.rows), dtype, a.codes, stream, "mx_matmul")
+    _launch("admmq_mx_matmul", a.device, stream, *a._ptrs(), *b._ptrs(), a.rows, b.rows, a.k,
+            MX_FORMATS[a.fmt], out.data_ptr(), DTYPES[dtype])
+    return out
+
+
+def mx_linear(x: torch.Tensor, w: MxTensor, dtype: torch.dtype | None = None,
+              tensor_scale: torch.Tensor | None = None, out: torch.Tensor | None = None,
+              stream=None) -> torch.Tensor:
+    """mx_matmul(mx_quantize(x, w.fmt, tensor_scale), w): a linear layer with
+    4-bit weights whose activations are quantised on the way in."""
+    q = mx_quantize(x, w.fmt, tensor_scale, stream)
+    return mx_matmul(q, w, dtype or x.dtype, out, stream)
 
 
 def project(wtilde, V, sigma, rsig, hdiag, bits, group, grid, codes, scale, zero, P_hi, P_lo,

@@ -11,12 +11,15 @@ import os
 import shutil
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libadmmq.so")
-SOURCES = ["admmq.cu"]
-HEADERS = ["ptx.cuh", "gemm.cuh", "kernels.cuh", "admm_loop.cuh", "gptq.cuh"]
+SOURCES = ["admmq.cu", "mx.cu", "packed.cu"]
+HEADERS = ["host.cuh", "ptx.cuh", "gemm.cuh", "kernels.cuh", "admm_loop.cuh", "gptq.cuh", "mx.cuh",
+           "product.cuh"]
 INCLUDE = os.path.join(os.path.dirname(HERE), "include", "admmq.h")
 
 
@@ -35,26 +38,39 @@ def _stale() -> bool:
     return any(os.path.getmtime(p) > t for p in deps)
 
 
-def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
-    if not force and not _stale():
-        return LIB
-    nvcc = _nvcc()
-    cuda_home = os.path.dirname(os.path.dirname(nvcc))
-    libdir = os.path.join(cuda_home, "lib64")
-    cmd = [nvcc, "-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", "-std=c++17",
-           "-Xcompiler", "-fPIC,-O2", "-shared", "--expt-relaxed-constexpr",
-           "-o", LIB + ".tmp"] + [os.path.join(CSRC, s) for s in SOURCES] + [
-           "-L" + libdir, "-lcusolver", "-lcublas", "-Xlinker", "-rpath," + libdir]
-    if ptxas_info:
-        cmd += ["-Xptxas", "-v"]
+def _run(cmd, verbose: bool) -> int:
     if verbose:
         print(" ".join(cmd), flush=True)
     res = subprocess.run(cmd, capture_output=True, text=True)
     if verbose or res.returncode != 0:
         sys.stdout.write(res.stdout)
         sys.stderr.write(res.stderr)
-    if res.returncode != 0:
-        raise RuntimeError(f"nvcc failed with exit code {res.returncode}")
+    return res.returncode
+
+
+def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
+    if not force and not _stale():
+        return LIB
+    nvcc = _nvcc()
+    cuda_home = os.path.dirname(os.path.dirname(nvcc))
+    libdir = os.path.join(cuda_home, "lib64")
+    flags = ["-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", "-std=c++17",
+             "-Xcompiler", "-fPIC,-O2", "--expt-relaxed-constexpr"]
+    if ptxas_info:
+        flags += ["-Xptxas", "-v"]
+    with tempfile.TemporaryDirectory(dir=HERE, prefix=".build_") as tmp:
+        # the sources are compiled side by side, then linked
+        objs = [os.path.join(tmp, s + ".o") for s in SOURCES]
+        cmds = [[nvcc] + flags + ["-c", "-o", o, os.path.join(CSRC, s)]
+                for s, o in zip(SOURCES, objs)]
+        link = [nvcc] + flags + ["-shared", "-o", LIB + ".tmp"] + objs + [
+            "-L" + libdir, "-lcusolver", "-lcublas", "-Xlinker", "-rpath," + libdir]
+        with ThreadPoolExecutor(len(cmds)) as pool:
+            for res in pool.map(lambda c: _run(c, verbose), cmds):
+                if res:
+                    raise RuntimeError(f"nvcc failed with exit code {res}")
+        if _run(link, verbose):
+            raise RuntimeError("linking failed")
     os.replace(LIB + ".tmp", LIB)
     return LIB
 

@@ -16,7 +16,7 @@
 #include <type_traits>
 #include <vector>
 
-#include "../../include/admmq.h"
+#include "host.cuh"
 #include "kernels.cuh"
 #include "admm_loop.cuh"
 
@@ -25,8 +25,6 @@ using namespace admmq;
 namespace {
 
 constexpr int kBM = 128;
-unsigned long long g_launches = 0;  // kernels launched by this library
-inline void count_launch() { __atomic_fetch_add(&g_launches, 1ull, __ATOMIC_RELAXED); }
 // X^T X: bf16, both operands MN-major (X is token-major).  Promoted every 8
 // k-blocks (32 MMAs of K = 16): measured 1226 TFLOP/s at q_proj against 1160
 // with 4 k-blocks; 16 gained nothing more.
@@ -613,26 +611,6 @@ __global__ void __launch_bounds__(STAGED ? 32 : 128) k_project(
 
 // ------------------------------------------------------------- host utils
 
-int num_sms() {
-  int dev = 0, n = 0;
-  cudaGetDevice(&dev);
-  cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-  return n > 0 ? n : 1;
-}
-
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  if (!fn) {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) ==
-            cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-  }
-  return fn;
-}
-
 // Row-major [outer][inner] tensor of fp32, bf16 or fp16, box {128 bytes,
 // box_outer}, 128-byte swizzle, out-of-bounds elements read as zero.
 bool make_map(CUtensorMap* m, const void* ptr, uint64_t inner, uint64_t outer, uint32_t box_outer,
@@ -663,8 +641,6 @@ bool make_plane_maps(CUtensorMap (&mp)[2], void* hi, void* lo, uint64_t d, uint6
   return make_map(&mp[0], hi, d, rows, box_rows, CU_TENSOR_MAP_DATA_TYPE_FLOAT32) &&
          make_map(&mp[1], lo, d, rows, box_rows, CU_TENSOR_MAP_DATA_TYPE_FLOAT32);
 }
-
-int cdiv(long long a, long long b) { return (int)((a + b - 1) / b); }
 
 // 128-row x BN tiles of an eigenbasis GEMM output [m][d] (per-tile partials)
 int eig_tiles(int m, int d) {
@@ -803,14 +779,6 @@ cudaError_t launch_eig(int enc, const CUtensorMap (&a)[2], const CUtensorMap (&b
   if (enc == ENC_F16) return launch_gemm<EigCfgF, EpiF>(a[0], a[1], b[0], b[1], g, ep, st);
   if (enc == ENC_MIX) return launch_gemm<EigCfg, EpiM>(a[0], a[1], b[0], b[1], g, ep, st);
   return launch_gemm<EigCfg3, Epi3>(a[0], a[1], b[0], b[1], g, ep, st);
-}
-
-int device_ok() {
-  int dev = 0, major = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return ADMMQ_ERR_CUDA;
-  if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess)
-    return ADMMQ_ERR_CUDA;
-  return major == 10 ? ADMMQ_OK : ADMMQ_ERR_UNSUPPORTED;
 }
 
 int grid_for(long long work, int per_block = 256) {
@@ -1052,11 +1020,6 @@ GptqLayout gptq_layout(int d, int m, int block, int lwork) {
   return L;
 }
 
-#define CK(x)                                      \
-  do {                                             \
-    if ((x) != cudaSuccess) return ADMMQ_ERR_CUDA; \
-  } while (0)
-
 // GEMM 1 and GEMM 2 of iterations t0 .. t0+count-1 in one launch.
 template <class Cfg, class E1, class E2>
 cudaError_t launch_admm_loop(const admmq_ctx* c, const GemmGeom& g, const TUpdateParams& p1,
@@ -1119,7 +1082,7 @@ const char* admmq_status_string(int s) {
   }
 }
 
-int admmq_version(void) { return 102; }
+int admmq_version(void) { return 103; }
 
 int64_t admmq_launch_count(void) { return (int64_t)__atomic_load_n(&g_launches, __ATOMIC_RELAXED); }
 

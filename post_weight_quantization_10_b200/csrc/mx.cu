@@ -1,0 +1,292 @@
+// mx.cu -- microscaled 4-bit floating point matrices (mxfp4, nvfp4):
+// quantisation, dequantisation and the product of two of them.
+#include "host.cuh"
+#include "mx.cuh"
+#include "product.cuh"
+
+using namespace admmq;
+
+namespace {
+
+// Eight consecutive elements of a row as fp32 (16 bytes of a 16-bit type, 32
+// of fp32; 16-byte aligned).
+__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
+  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+}
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8]) {
+  const uint4 a = *reinterpret_cast<const uint4*>(p);
+  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+  }
+}
+__device__ __forceinline__ void load8(const __half* p, float (&v)[8]) {
+  const uint4 a = *reinterpret_cast<const uint4*>(p);
+  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+    v[2 * i] = f.x;
+    v[2 * i + 1] = f.y;
+  }
+}
+__device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
+  reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+  reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+}
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8]) {
+  __nv_bfloat162 h[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+  *reinterpret_cast<uint4*>(p) = *reinterpret_cast<uint4*>(h);
+}
+__device__ __forceinline__ void store8(__half* p, const float (&v)[8]) {
+  __half2 h[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) h[i] = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+  *reinterpret_cast<uint4*>(p) = *reinterpret_cast<uint4*>(h);
+}
+
+// A block of threads takes 128 rows x 256 columns: the scale tiles it fills
+// (or reads) are whole and lie next to each other, 1 KB (mxfp4) or 2 KB
+// (nvfp4).  A warp takes a row at a time, a lane eight elements of it; the
+// four (two) lanes of a block find its largest magnitude by shuffles.
+constexpr int kSpan = 256;  // columns of a thread block
+constexpr int kMxThreads = 256;
+
+template <int FMT, typename T>
+__global__ void __launch_bounds__(kMxThreads)
+    k_mx_quantize(const T* __restrict__ x, long long rows, int k, long long ld, int spans,
+                  const float* __restrict__ tensor_scale, uint8_t* __restrict__ codes,
+                  uint8_t* __restrict__ scale) {
+  constexpr int TILE_K = MxFormat<FMT>::TILE_K;
+  constexpr int LANES = MxFormat<FMT>::BLOCK / 8;  // lanes that share a block
+  constexpr int TILES = kSpan / TILE_K;
+  __shared__ __align__(16) uint8_t tile[TILES * kScaleTile];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const long long row_tile = blockIdx.x / spans;
+  const int span = (int)(blockIdx.x - row_tile * spans);
+  const int col = span * kSpan + lane * 8;
+  const float g = FMT == MX_NVFP4 && tensor_scale ? *tensor_scale : 1.f;
+  for (int i = threadIdx.x; i < TILES * kScaleTile / 16; i += kMxThreads)
+    reinterpret_cast<uint4*>(tile)[i] = make_uint4(0, 0, 0, 0);
+  __syncthreads();
+#pragma unroll 4
+  for (int j = 0; j < 128 / (kMxThreads / 32); ++j) {
+    const int r = j * (kMxThreads / 32) + warp;
+    const long long row = row_tile * 128 + r;
+    // all lanes stay for the shuffles; a block's lanes are valid together
+    const bool valid = row < rows && col < k;
+    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (valid) load8(x + row * ld + col, v);
+    uint32_t amax = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) amax = max(amax, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+#pragma unroll
+    for (int o = LANES / 2; o > 0; o >>= 1) amax = max(amax, __shfl_xor_sync(~0u, amax, o));
+    const uint32_t byte = block_scale<FMT>(amax, g);
+    uint32_t out = 0;
+    if (amax < 0x7F800000u) {
+      if (FMT == MX_MXFP4) {
+        const float inv = e8m0_inverse(byte);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) out |= e2m1x2(v[2 * i] * inv, v[2 * i + 1] * inv) << (8 * i);
+      } else {
+        float t = block_step<FMT>(byte, g);
+        if (t > 0.f) {
+          // tiny steps: both sides times 2^64, so that 1 / t is finite
+          const float up = t < 0x1p-64f ? 0x1p64f : 1.f;
+          t *= up;
+          const float r1 = __frcp_rn(t);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            out |= e2m1x2(quotient_to_odd(v[2 * i] * up, t, r1),
+                          quotient_to_odd(v[2 * i + 1] * up, t, r1))
+                   << (8 * i);
+        }
+      }
+    }
+    if (valid) {
+      *reinterpret_cast<uint32_t*>(codes + (row * k + col) / 2) = out;
+      if (lane % LANES == 0) {
+        const int c = lane / LANES;
+        tile[(c >> 2) * kScaleTile + scale_at(r, c & 3)] = (uint8_t)byte;
+      }
+    }
+  }
+  __syncthreads();
+  const int col_tiles = (k + TILE_K - 1) / TILE_K;
+  const int here = min(TILES, col_tiles - span * TILES);
+  uint4* dst = reinterpret_cast<uint4*>(scale + (row_tile * col_tiles + span * TILES) * kScaleTile);
+  for (int i = threadIdx.x; i < here * kScaleTile / 16; i += kMxThreads)
+    dst[i] = reinterpret_cast<const uint4*>(tile)[i];
+}
+
+template <int FMT, typename T>
+__global__ void __launch_bounds__(kMxThreads)
+    k_mx_dequantize(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scale,
+                    long long rows, int k, int spans, const float* __restrict__ tensor_scale,
+                    T* __restrict__ out, long long ld) {
+  constexpr int TILE_K = MxFormat<FMT>::TILE_K;
+  constexpr int LANES = MxFormat<FMT>::BLOCK / 8;
+  constexpr int TILES = kSpan / TILE_K;
+  __shared__ __align__(16) uint8_t tile[TILES * kScaleTile];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const long long row_tile = blockIdx.x / spans;
+  const int span = (int)(blockIdx.x - row_tile * spans);
+  const int col = span * kSpan + lane * 8;
+  const float g = FMT == MX_NVFP4 && tensor_scale ? *tensor_scale : 1.f;
+  const int col_tiles = (k + TILE_K - 1) / TILE_K;
+  const int here = min(TILES, col_tiles - span * TILES);
+  const uint4* src =
+      reinterpret_cast<const uint4*>(scale + (row_tile * col_tiles + span * TILES) * kScaleTile);
+  for (int i = threadIdx.x; i < here * kScaleTile / 16; i += kMxThreads)
+    reinterpret_cast<uint4*>(tile)[i] = src[i];
+  __syncthreads();
+  if (col >= k) return;
+  const int c = lane / LANES;
+#pragma unroll 8
+  for (int j = 0; j < 128 / (kMxThreads / 32); ++j) {
+    const int r = j * (kMxThreads / 32) + warp;
+    const long long row = row_tile * 128 + r;
+    if (row >= rows) break;
+    const uint32_t in = *reinterpret_cast<const uint32_t*>(codes + (row * k + col) / 2);
+    const float t = block_step<FMT>(tile[(c >> 2) * kScaleTile + scale_at(r, c & 3)], g);
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = e2m1x2_values((in >> (8 * i)) & 0xFFu);
+      v[2 * i] = f.x * t;
+      v[2 * i + 1] = f.y * t;
+    }
+    store8(out + row * ld + col, v);
+  }
+}
+
+// Element (row, k) of an MX matrix without the tensor scale, for k_product.
+template <int FMT>
+struct MxElement {
+  const uint8_t *codes, *scale;
+  int col_tiles, half_k;
+  __device__ __forceinline__ float operator()(long long row, int k) const {
+    constexpr int TILE_K = MxFormat<FMT>::TILE_K, BLOCK = MxFormat<FMT>::BLOCK;
+    const uint32_t b = codes[row * half_k + (k >> 1)];
+    const float2 f = e2m1x2_values(b);
+    const uint8_t s = scale[((row >> 7) * col_tiles + k / TILE_K) * kScaleTile +
+                            scale_at((int)(row & 127), k % TILE_K / BLOCK)];
+    return ((k & 1) ? f.y : f.x) * block_step<FMT>(s, 1.f);
+  }
+};
+
+bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
+bool mx_shape_ok(int64_t rows, int k, int fmt) {
+  return rows >= 0 && rows <= (1ll << 30) && k > 0 && k % 32 == 0 && k <= (1 << 24) &&
+         (fmt == ADMMQ_MX_MXFP4 || fmt == ADMMQ_MX_NVFP4);
+}
+int mx_tile_k(int fmt) { return fmt == ADMMQ_MX_MXFP4 ? 128 : 64; }
+int dtype_size(int dtype) { return dtype == ADMMQ_DTYPE_F32 ? 4 : 2; }
+bool dtype_ok(int dtype) { return dtype >= ADMMQ_DTYPE_F32 && dtype <= ADMMQ_DTYPE_F16; }
+
+}  // namespace
+
+// Calls BODY(FMT, T) with the format and element type of the arguments.
+#define MX_DISPATCH_T(FMT, dtype, BODY)                  \
+  if ((dtype) == ADMMQ_DTYPE_F32) {                      \
+    BODY(FMT, float);                                    \
+  } else if ((dtype) == ADMMQ_DTYPE_BF16) {              \
+    BODY(FMT, __nv_bfloat16);                            \
+  } else {                                               \
+    BODY(FMT, __half);                                   \
+  }
+#define MX_DISPATCH(fmt, dtype, BODY)                    \
+  if ((fmt) == ADMMQ_MX_MXFP4) {                         \
+    MX_DISPATCH_T(MX_MXFP4, dtype, BODY)                 \
+  } else {                                               \
+    MX_DISPATCH_T(MX_NVFP4, dtype, BODY)                 \
+  }
+
+extern "C" {
+
+size_t admmq_mx_scale_bytes(int64_t rows, int k, int fmt) {
+  if (!mx_shape_ok(rows, k, fmt)) return 0;
+  return (size_t)((rows + 127) / 128) * (size_t)cdiv(k, mx_tile_k(fmt)) * kScaleTile;
+}
+
+int admmq_mx_quantize(const void* x, int x_dtype, int64_t rows, int k, int64_t ld, int fmt,
+                      const float* tensor_scale, uint8_t* codes, uint8_t* scale, void* stream) {
+  if (!mx_shape_ok(rows, k, fmt) || !dtype_ok(x_dtype) || ld < k) return ADMMQ_ERR_INVALID_ARG;
+  if (fmt == ADMMQ_MX_MXFP4 && tensor_scale) return ADMMQ_ERR_INVALID_ARG;
+  if (((uintptr_t)tensor_scale & 3) != 0) return ADMMQ_ERR_INVALID_ARG;
+  if (rows == 0) return ADMMQ_OK;
+  if (!x || !codes || !scale || !aligned16(x) || !aligned16(codes) || !aligned16(scale) ||
+      ld * dtype_size(x_dtype) % 16 != 0)
+    return ADMMQ_ERR_INVALID_ARG;
+  int rc = device_ok();
+  if (rc) return rc;
+  const int spans = cdiv(k, kSpan);
+  const long long grid = (rows + 127) / 128 * spans;
+  if (grid > 0x7FFFFFFFll) return ADMMQ_ERR_UNSUPPORTED;
+#define QUANTIZE(FMT, T)                                                                         \
+  count_launch(), k_mx_quantize<FMT, T><<<(unsigned)grid, kMxThreads, 0, (cudaStream_t)stream>>>( \
+                      (const T*)x, rows, k, ld, spans, tensor_scale, codes, scale)
+  MX_DISPATCH(fmt, x_dtype, QUANTIZE)
+#undef QUANTIZE
+  CK(cudaGetLastError());
+  return ADMMQ_OK;
+}
+
+int admmq_mx_dequantize(const uint8_t* codes, const uint8_t* scale, int64_t rows, int k, int fmt,
+                        const float* tensor_scale, void* out, int out_dtype, int64_t ld,
+                        void* stream) {
+  if (!mx_shape_ok(rows, k, fmt) || !dtype_ok(out_dtype) || ld < k) return ADMMQ_ERR_INVALID_ARG;
+  if (fmt == ADMMQ_MX_MXFP4 && tensor_scale) return ADMMQ_ERR_INVALID_ARG;
+  if (((uintptr_t)tensor_scale & 3) != 0) return ADMMQ_ERR_INVALID_ARG;
+  if (rows == 0) return ADMMQ_OK;
+  if (!out || !codes || !scale || !aligned16(out) || !aligned16(codes) || !aligned16(scale) ||
+      ld * dtype_size(out_dtype) % 16 != 0)
+    return ADMMQ_ERR_INVALID_ARG;
+  int rc = device_ok();
+  if (rc) return rc;
+  const int spans = cdiv(k, kSpan);
+  const long long grid = (rows + 127) / 128 * spans;
+  if (grid > 0x7FFFFFFFll) return ADMMQ_ERR_UNSUPPORTED;
+#define DEQUANTIZE(FMT, T)                                                                     \
+  count_launch(),                                                                              \
+      k_mx_dequantize<FMT, T><<<(unsigned)grid, kMxThreads, 0, (cudaStream_t)stream>>>(        \
+          codes, scale, rows, k, spans, tensor_scale, (T*)out, ld)
+  MX_DISPATCH(fmt, out_dtype, DEQUANTIZE)
+#undef DEQUANTIZE
+  CK(cudaGetLastError());
+  return ADMMQ_OK;
+}
+
+int admmq_mx_matmul(const uint8_t* a_codes, const uint8_t* a_scale, const float* a_tensor_scale,
+                    const uint8_t* b_codes, const uint8_t* b_scale, const float* b_tensor_scale,
+                    int64_t m, int n, int k, int fmt, void* out, int out_dtype, void* stream) {
+  if (!mx_shape_ok(m, k, fmt) || !mx_shape_ok(n, k, fmt) || n < 1 || !dtype_ok(out_dtype))
+    return ADMMQ_ERR_INVALID_ARG;
+  if (fmt == ADMMQ_MX_MXFP4 && (a_tensor_scale || b_tensor_scale)) return ADMMQ_ERR_INVALID_ARG;
+  if ((((uintptr_t)a_tensor_scale | (uintptr_t)b_tensor_scale) & 3) != 0)
+    return ADMMQ_ERR_INVALID_ARG;
+  if (m == 0) return ADMMQ_OK;
+  if (!a_codes || !a_scale || !b_codes || !b_scale || !out || !aligned16(a_codes) ||
+      !aligned16(a_scale) || !aligned16(b_codes) || !aligned16(b_scale) || !aligned16(out))
+    return ADMMQ_ERR_INVALID_ARG;
+  int rc = device_ok();
+  if (rc) return rc;
+  const int ct = cdiv(k, mx_tile_k(fmt));
+#define PRODUCT(FMT, T)                                                                       \
+  launch_product<T>(MxElement<FMT>{a_codes, a_scale, ct, k / 2},                              \
+                    MxElement<FMT>{b_codes, b_scale, ct, k / 2}, (int)m, n, k, a_tensor_scale, \
+                    b_tensor_scale, (T*)out, (cudaStream_t)stream)
+  MX_DISPATCH(fmt, out_dtype, PRODUCT)
+#undef PRODUCT
+  CK(cudaGetLastError());
+  return ADMMQ_OK;
+}
+
+}  // extern "C"
