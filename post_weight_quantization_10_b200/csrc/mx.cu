@@ -2,7 +2,7 @@
 // quantisation, dequantisation and the product of two of them.
 #include "host.cuh"
 #include "mx.cuh"
-#include "product.cuh"
+#include "mx_gemm.cuh"
 
 using namespace admmq;
 
@@ -167,21 +167,6 @@ __global__ void __launch_bounds__(kMxThreads)
   }
 }
 
-// Element (row, k) of an MX matrix without the tensor scale, for k_product.
-template <int FMT>
-struct MxElement {
-  const uint8_t *codes, *scale;
-  int col_tiles, half_k;
-  __device__ __forceinline__ float operator()(long long row, int k) const {
-    constexpr int TILE_K = MxFormat<FMT>::TILE_K, BLOCK = MxFormat<FMT>::BLOCK;
-    const uint32_t b = codes[row * half_k + (k >> 1)];
-    const float2 f = e2m1x2_values(b);
-    const uint8_t s = scale[((row >> 7) * col_tiles + k / TILE_K) * kScaleTile +
-                            scale_at((int)(row & 127), k % TILE_K / BLOCK)];
-    return ((k & 1) ? f.y : f.x) * block_step<FMT>(s, 1.f);
-  }
-};
-
 bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
 bool mx_shape_ok(int64_t rows, int k, int fmt) {
   return rows >= 0 && rows <= (1ll << 30) && k > 0 && k % 32 == 0 && k <= (1 << 24) &&
@@ -189,6 +174,67 @@ bool mx_shape_ok(int64_t rows, int k, int fmt) {
 }
 int mx_tile_k(int fmt) { return fmt == ADMMQ_MX_MXFP4 ? 128 : 64; }
 int dtype_size(int dtype) { return dtype == ADMMQ_DTYPE_F32 ? 4 : 2; }
+// Codes [rows][k / 2] in boxes of 128 bytes x box_rows, 128-byte swizzle,
+// bytes out of range read as zero (the code of 0).
+bool make_codes_map(CUtensorMap* m, const void* ptr, int k, int64_t rows, int box_rows) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[2] = {(cuuint64_t)k / 2, (cuuint64_t)rows};
+  cuuint64_t strides[1] = {(cuuint64_t)k / 2};
+  cuuint32_t box[2] = {128, (cuuint32_t)box_rows};
+  cuuint32_t estr[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(ptr), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Shared memory to ask for, so that blocks which fit an SM together never ask
+// for more than its 512 tensor-memory columns: the CTAs of a cluster wait for
+// one another, and one of them that waited for columns held by another cluster
+// could close a circle.  Columns and shared memory (228 KB with 1 KB a block)
+// run out together; the 40 KB keep it off the SMs of the layer solve's engine,
+// whose blocks hold all columns and leave 29 KB.
+int tmem_fair_smem(int bytes, int cols) {
+  const int fair = cols * (228 * 1024 / 512) - 1024;
+  if (bytes < fair) bytes = fair;
+  return bytes < 40 * 1024 ? 40 * 1024 : bytes;
+}
+
+template <int FMT, typename T>
+int launch_tile(MxArgs& p, cudaStream_t st) {
+  constexpr int NSF = kMxBK / MxFormat<FMT>::TILE_K;
+  const int xt = (p.tn + 127) / 128, tiles = p.tiles_n * (p.tn < 128 ? 1 : cdiv(p.m, p.tn));
+  int ranks = 1;
+  while (ranks < 8 && 2 * ranks <= p.kblocks && tiles * 2 * ranks <= 2 * num_sms()) ranks *= 2;
+  p.stage_bytes = 128 * 128 + ((p.tn * 128 + 1023) & ~1023) + (((1 + xt) * NSF * kScaleTile + 1023) & ~1023);
+  const int blocks = cdiv(p.kblocks, ranks);
+  p.stages = 200 * 1024 / p.stage_bytes;
+  if (p.stages > blocks) p.stages = blocks;
+  p.bar_off = p.stages * p.stage_bytes;
+  if (ranks > 1 && p.bar_off < p.tn * 512) p.bar_off = p.tn * 512;
+  const int cols = ((p.tn + 31) & ~31) + 4 * NSF * (1 + xt);
+  p.tmem_cols = 32;
+  while (p.tmem_cols < cols) p.tmem_cols *= 2;
+  const int smem = tmem_fair_smem(p.bar_off + 1024 + 16 * p.stages + 64, p.tmem_cols);
+  auto kern = k_mx_tile<FMT, T>;
+  CK(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+  cudaLaunchConfig_t lc = {};
+  lc.gridDim = dim3((unsigned)(tiles * ranks));
+  lc.blockDim = dim3(kMxTileThreads);
+  lc.dynamicSmemBytes = smem;
+  lc.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = ranks;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  lc.attrs = attr;
+  lc.numAttrs = 1;
+  count_launch();
+  CK(cudaLaunchKernelEx(&lc, kern, p));
+  return ADMMQ_OK;
+}
+
 bool dtype_ok(int dtype) { return dtype >= ADMMQ_DTYPE_F32 && dtype <= ADMMQ_DTYPE_F16; }
 
 }  // namespace
@@ -278,15 +324,25 @@ int admmq_mx_matmul(const uint8_t* a_codes, const uint8_t* a_scale, const float*
     return ADMMQ_ERR_INVALID_ARG;
   int rc = device_ok();
   if (rc) return rc;
-  const int ct = cdiv(k, mx_tile_k(fmt));
-#define PRODUCT(FMT, T)                                                                       \
-  launch_product<T>(MxElement<FMT>{a_codes, a_scale, ct, k / 2},                              \
-                    MxElement<FMT>{b_codes, b_scale, ct, k / 2}, (int)m, n, k, a_tensor_scale, \
-                    b_tensor_scale, (T*)out, (cudaStream_t)stream)
+  MxArgs p;
+  p.w_scale = b_scale;
+  p.x_scale = a_scale;
+  p.gw = b_tensor_scale;
+  p.gx = a_tensor_scale;
+  p.out = out;
+  p.m = (int)m;
+  p.n = n;
+  p.k = k;
+  p.tn = m <= 128 ? ((int)m + 15) / 16 * 16 : 256;
+  p.tiles_n = cdiv(n, 128);
+  p.kblocks = cdiv(k, kMxBK);
+  p.col_tiles = cdiv(k, mx_tile_k(fmt));
+  if (!make_codes_map(&p.w, b_codes, k, n, 128) || !make_codes_map(&p.x, a_codes, k, m, p.tn))
+    return ADMMQ_ERR_CUDA;
+#define PRODUCT(FMT, T) rc = launch_tile<FMT, T>(p, (cudaStream_t)stream)
   MX_DISPATCH(fmt, out_dtype, PRODUCT)
 #undef PRODUCT
-  CK(cudaGetLastError());
-  return ADMMQ_OK;
+  return rc;
 }
 
 }  // extern "C"

@@ -1,0 +1,249 @@
+// mx_gemm.cuh -- product of two microscaled 4-bit matrices on the block-scaled
+// tensor cores: out[i][j] = g_a g_b sum_k a[i][k] b[j][k].
+//
+// The weights b are the MMA's first operand (128 output columns j on the 128
+// tensor-memory lanes), the activations a its second (up to 256 tokens i): few
+// tokens then cost few columns, and a warp's lanes hold neighbouring columns j
+// of one token, which out stores next to each other.
+#pragma once
+#include "mx.cuh"
+#include "ptx.cuh"
+
+namespace admmq {
+
+// ------------------------------------------------------------- PTX wrappers
+
+// Untiled asynchronous copy global -> shared (16-byte aligned, size a multiple
+// of 16), completing on an mbarrier.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
+                                          uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          dst),
+      "l"(src), "r"(bytes), "r"(bar)
+      : "memory");
+}
+
+// One scale tile (512 bytes: 32 rows of 16 bytes) from shared memory to four
+// tensor-memory columns, repeated in the four lane quarters.
+__device__ __forceinline__ void tmem_copy_scales(uint32_t taddr, uint64_t desc) {
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc)
+               : "memory");
+}
+// Its descriptor: no swizzle, groups of 8 rows 128 bytes apart.
+__device__ __forceinline__ uint64_t scale_desc(uint32_t saddr) {
+  return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)(128 >> 4) << 32) | ((uint64_t)1 << 46);
+}
+
+// D[tmem] (+)= A[smem] B[smem], e2m1 elements, K = 64: scales per 32 (e8m0) or
+// per 16 elements (e4m3) from tensor memory.
+template <int FMT>
+__device__ __forceinline__ void mma_mx(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                       uint32_t idesc, uint32_t sfa, uint32_t sfb,
+                                       uint32_t accumulate) {
+  if (FMT == MX_MXFP4)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], "
+        "[%5], p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, "
+        "[%4], [%5], p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+}
+
+// Instruction descriptor: e2m1 x e2m1, scale type, M rows and N columns; sf:
+// which byte pair of the scale words the K = 64 step takes (mxfp4: 0 or 2).
+template <int FMT>
+__device__ __forceinline__ uint32_t idesc_mx(int M, int N, uint32_t sf) {
+  return (sf << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) |
+         (FMT == MX_MXFP4 ? 1u << 23 : 0u) | ((uint32_t)(M >> 7) << 27) | (sf << 29);
+}
+
+__device__ __forceinline__ float ld_cluster_f32(uint32_t addr_cluster) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr_cluster) : "memory");
+  return v;
+}
+
+__device__ __forceinline__ void put(float* p, float v) { *p = v; }
+__device__ __forceinline__ void put(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+__device__ __forceinline__ void put(__half* p, float v) { *p = __float2half_rn(v); }
+
+// ------------------------------------------------------------------- kernel
+
+struct MxArgs {
+  CUtensorMap w, x;            // codes of the weights and of the activations
+  const uint8_t *w_scale, *x_scale;
+  const float *gw, *gx;        // tensor scales or null
+  void* out;
+  int m, n, k;                 // tokens, output columns, reduction
+  int tn;                      // tokens of a tile: a multiple of 16 up to 128 that holds all
+                               // of them, or 128 or 256 (tiles start at a scale tile's row 0)
+  int tiles_n;                 // 128-column tiles
+  int kblocks, col_tiles;      // 256-element stages; scale tiles along k
+  int stages, stage_bytes, bar_off;
+  int tmem_cols;
+};
+
+constexpr int kMxBK = 256;  // elements of K per stage: 128-byte rows
+constexpr int kMxTileThreads = 192;
+
+// One output tile of 128 columns x tn tokens per cluster; the cluster's CTAs
+// share the reduction (contiguous ranges of stages) and add their partial
+// tiles through distributed shared memory, in rank order.
+//   warp 0  TMA producer    warp 1  MMA issuer    warps 2-5  epilogue
+template <int FMT, typename T>
+__global__ void __launch_bounds__(kMxTileThreads)
+    k_mx_tile(const __grid_constant__ MxArgs p) {
+  constexpr int NSF = kMxBK / MxFormat<FMT>::TILE_K;  // scale tiles per stage and 128 rows
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  const int xt = (p.tn + 127) >> 7;  // 128-row scale tiles of the activations
+  const int x_bytes = p.tn * 128;
+  const int x_off = 128 * 128, sw_off = x_off + ((x_bytes + 1023) & ~1023),
+            sx_off = sw_off + NSF * kScaleTile;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + p.bar_off);
+  uint64_t* empty = full + p.stages;
+  uint64_t* done = empty + p.stages;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint32_t rank, ranks;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(ranks));
+  const long long tile = blockIdx.x / ranks;
+  const int tn_tile = (int)(tile % p.tiles_n), tm_tile = (int)(tile / p.tiles_n);
+  const int kb0 = (int)((long long)rank * p.kblocks / ranks);
+  const int kb1 = (int)((long long)(rank + 1) * p.kblocks / ranks);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < p.stages; ++s) {
+      mbar_init(smem_u32(&full[s]), 1);
+      mbar_init(smem_u32(&empty[s]), 1);
+    }
+    mbar_init(smem_u32(done), 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) tmem_alloc(smem_u32(tmem_slot), p.tmem_cols);
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      bool ok = true;
+      int it = 0;
+      for (int kb = kb0; kb < kb1; ++kb, ++it) {
+        const int s = it % p.stages;
+        if (it >= p.stages &&
+            !mbar_wait(smem_u32(&empty[s]), (uint32_t)(it / p.stages - 1) & 1u, abort_flag, nullptr)) {
+          ok = false;
+          break;
+        }
+        const uint32_t bar = smem_u32(&full[s]), st = smem_u32(smem + s * p.stage_bytes);
+        const int sf = min(NSF, p.col_tiles - kb * NSF) * kScaleTile;  // scale bytes of this stage
+        // a token tile's 128-row scale tiles that exist
+        const int xrows = min(xt, (p.m + 127) / 128 - (tm_tile * p.tn >> 7));
+        mbar_arrive_expect_tx(bar, 128 * 128 + x_bytes + sf * (1 + xrows));
+        tma_load_2d(st, &p.w, kb * 128, tn_tile * 128, bar);
+        tma_load_2d(st + x_off, &p.x, kb * 128, tm_tile * p.tn, bar);
+        bulk_load(st + sw_off, p.w_scale + ((long long)tn_tile * p.col_tiles + kb * NSF) * kScaleTile,
+                  sf, bar);
+        for (int i = 0; i < xrows; ++i)
+          bulk_load(st + sx_off + i * NSF * kScaleTile,
+                    p.x_scale + (((long long)(tm_tile * p.tn >> 7) + i) * p.col_tiles + kb * NSF) *
+                                    kScaleTile,
+                    sf, bar);
+      }
+      if (!ok)
+        for (int j = max(0, it - p.stages); j < it; ++j)
+          mbar_wait_drain(smem_u32(&full[j % p.stages]), (uint32_t)(j / p.stages) & 1u);
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      const uint32_t sfw = tmem + ((p.tn + 31) & ~31), sfx = sfw + 4 * NSF;
+      for (int kb = kb0, it = 0; kb < kb1; ++kb, ++it) {
+        const int s = it % p.stages;
+        if (!mbar_wait(smem_u32(&full[s]), (uint32_t)(it / p.stages) & 1u, abort_flag, nullptr)) break;
+        tc_fence_after();
+        const uint32_t st = smem_u32(smem + s * p.stage_bytes);
+        const uint64_t dw = smem_desc_sw128(st, 16, 1024), dx = smem_desc_sw128(st + x_off, 16, 1024);
+        const int steps = min(4, (p.k - kb * kMxBK + 63) / 64);
+        const int tiles = min(NSF, p.col_tiles - kb * NSF);
+        for (int i = 0; i < tiles; ++i) {
+          tmem_copy_scales(sfw + 4 * i, scale_desc(st + sw_off + i * kScaleTile));
+          for (int j = 0; j < xt; ++j)
+            tmem_copy_scales(sfx + 4 * (i * xt + j),
+                             scale_desc(st + sx_off + (j * NSF + i) * kScaleTile));
+        }
+        for (int j = 0; j < steps; ++j) {
+          const int at = FMT == MX_MXFP4 ? j >> 1 : j;
+          const uint32_t sf = FMT == MX_MXFP4 ? 2u * (j & 1) : 0u;
+          mma_mx<FMT>(tmem, dw + 2 * j, dx + 2 * j, idesc_mx<FMT>(128, p.tn, sf), sfw + 4 * at,
+                      sfx + 4 * at * xt, (it > 0 || j > 0) ? 1u : 0u);
+        }
+        mma_commit(smem_u32(&empty[s]));
+      }
+      mma_commit(smem_u32(done));
+    }
+  }
+  __syncwarp();
+  // ------------------------------------------------------------- epilogue
+  const int row = (warp & 3) * 32 + lane;  // column of the output tile
+  const uint32_t ta = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+  float* part = reinterpret_cast<float*>(smem);  // [tn][128], over the drained stages
+  bool ok = true;
+  const long long col = (long long)tn_tile * 128 + row;
+  const int tokens = min(p.tn, p.m - tm_tile * p.tn);
+  const float g = (p.gw ? *p.gw : 1.f) * (p.gx ? *p.gx : 1.f);
+  T* out = reinterpret_cast<T*>(p.out) + (long long)tm_tile * p.tn * p.n + col;
+  if (warp >= 2) {
+    ok = mbar_wait(smem_u32(done), 0, abort_flag, nullptr);
+    ok = __all_sync(~0u, ok) && !*abort_flag;
+    tc_fence_after();
+    for (int c = 0; c < p.tn; c += 16) {
+      float v[16];
+      tmem_ld16(ta + c, v);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        if (!ok) v[i] = __int_as_float(0x7FFFFFFF);
+        if (ranks > 1)
+          part[(c + i) * 128 + row] = v[i];
+        else if (col < p.n && c + i < tokens)
+          put(out + (long long)(c + i) * p.n, v[i] * g);
+      }
+    }
+    tc_fence_before();
+  }
+  if (ranks > 1) {
+    cluster_sync();
+    if (warp >= 2 && col < p.n) {
+      const int c0 = (int)(rank * p.tn / ranks), c1 = min((int)((rank + 1) * p.tn / ranks), tokens);
+      for (int c = c0; c < c1; ++c) {
+        float v = 0.f;
+        for (uint32_t r = 0; r < ranks; ++r)
+          v += ld_cluster_f32(cluster_addr(smem_u32(part + c * 128 + row), r));
+        put(out + (long long)c * p.n, v * g);
+      }
+    }
+    cluster_sync();
+  }
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, p.tmem_cols);
+  }
+}
+
+}  // namespace admmq
