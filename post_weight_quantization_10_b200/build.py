@@ -19,7 +19,7 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libadmmq.so")
 SOURCES = ["admmq.cu", "mx.cu", "packed.cu"]
 HEADERS = ["host.cuh", "ptx.cuh", "gemm.cuh", "kernels.cuh", "admm_loop.cuh", "gptq.cuh", "mx.cuh",
-           "mx_gemm.cuh", "product.cuh"]
+           "mx_gemm.cuh", "packed.cuh", "packed_few.cuh", "product.cuh"]
 INCLUDE = os.path.join(os.path.dirname(HERE), "include", "admmq.h")
 
 
