@@ -1,0 +1,26 @@
+// async.cuh -- further PTX wrappers of the quantised-weight products: bulk
+// copies and reads of a cluster's shared memory.
+#pragma once
+#include <stdint.h>
+
+namespace admmq {
+
+// Untiled asynchronous copy global -> shared (16-byte aligned, size a multiple
+// of 16), completing on an mbarrier.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
+                                          uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          dst),
+      "l"(src), "r"(bytes), "r"(bar)
+      : "memory");
+}
+
+// A float in the shared memory of a CTA of the cluster.
+__device__ __forceinline__ float ld_cluster_f32(uint32_t addr_cluster) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr_cluster) : "memory");
+  return v;
+}
+
+}  // namespace admmq

@@ -6,23 +6,13 @@
 // tokens then cost few columns, and a warp's lanes hold neighbouring columns j
 // of one token, which out stores next to each other.
 #pragma once
+#include "async.cuh"
 #include "mx.cuh"
 #include "ptx.cuh"
 
 namespace admmq {
 
 // ------------------------------------------------------------- PTX wrappers
-
-// Untiled asynchronous copy global -> shared (16-byte aligned, size a multiple
-// of 16), completing on an mbarrier.
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
-                                          uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-          dst),
-      "l"(src), "r"(bytes), "r"(bar)
-      : "memory");
-}
 
 // One scale tile (512 bytes: 32 rows of 16 bytes) from shared memory to four
 // tensor-memory columns, repeated in the four lane quarters.
@@ -65,12 +55,6 @@ template <int FMT>
 __device__ __forceinline__ uint32_t idesc_mx(int M, int N, uint32_t sf) {
   return (sf << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) |
          (FMT == MX_MXFP4 ? 1u << 23 : 0u) | ((uint32_t)(M >> 7) << 27) | (sf << 29);
-}
-
-__device__ __forceinline__ float ld_cluster_f32(uint32_t addr_cluster) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr_cluster) : "memory");
-  return v;
 }
 
 __device__ __forceinline__ void put(float* p, float v) { *p = v; }

@@ -32,33 +32,48 @@ struct PackedElement {
   }
 };
 
-// Tokens up to which the weights go straight into registers.
-constexpr int kFewTokens = 16;
+// Tokens that the mma.sync kernel takes.
+constexpr int kFewTokens = 32;
 
-template <typename X>
-const void* few_kernel(int m, int bits) {
-  static const void* const one[8] = {
-      (const void*)k_packed_few<X, 1, 1>, (const void*)k_packed_few<X, 1, 2>,
-      (const void*)k_packed_few<X, 1, 3>, (const void*)k_packed_few<X, 1, 4>,
-      (const void*)k_packed_few<X, 1, 5>, (const void*)k_packed_few<X, 1, 6>,
-      (const void*)k_packed_few<X, 1, 7>, (const void*)k_packed_few<X, 1, 8>};
-  static const void* const two[8] = {
-      (const void*)k_packed_few<X, 2, 1>, (const void*)k_packed_few<X, 2, 2>,
-      (const void*)k_packed_few<X, 2, 3>, (const void*)k_packed_few<X, 2, 4>,
-      (const void*)k_packed_few<X, 2, 5>, (const void*)k_packed_few<X, 2, 6>,
-      (const void*)k_packed_few<X, 2, 7>, (const void*)k_packed_few<X, 2, 8>};
-  return (m <= 8 ? one : two)[bits - 1];
+template <typename X, int NT, int RT>
+const void* few_kernel(int bits) {
+  static const void* const table[8] = {
+      (const void*)k_packed_few<X, NT, RT, 1>, (const void*)k_packed_few<X, NT, RT, 2>,
+      (const void*)k_packed_few<X, NT, RT, 3>, (const void*)k_packed_few<X, NT, RT, 4>,
+      (const void*)k_packed_few<X, NT, RT, 5>, (const void*)k_packed_few<X, NT, RT, 6>,
+      (const void*)k_packed_few<X, NT, RT, 7>, (const void*)k_packed_few<X, NT, RT, 8>};
+  return table[bits - 1];
 }
 
 template <typename X>
-int launch_few(const PackedArgs& p, cudaStream_t st) {
-  const int blocks = cdiv(p.n, kFewRows), spans = cdiv(p.k, 128);
-  // enough blocks for three on each SM, each with a span for every warp
-  int ranks = 1;
-  while (ranks < 8 && blocks * 2 * ranks <= 3 * num_sms() && spans >= 16 * ranks) ranks *= 2;
+int launch_few(PackedArgs p, cudaStream_t st) {
+  const int spans = cdiv(p.k, 128);
+  // all activations next to two stages in a third of the shared memory?
+  const bool one = p.m <= 8 && (long long)p.m * (spans * 256 + 64) <= 34 * 1024;
+  const int rows = one ? 16 : 64, blocks = cdiv(p.n, rows);
+  int ranks = 1, shift = 0;
+  if (!one)
+    while (ranks < 8 && blocks * 2 * ranks <= 4 * num_sms() && spans >= 4 * ranks) ranks *= 2, ++shift;
+  const int range = cdiv(spans, ranks), most = one ? 32 : 8;
+  int per = 1;
+  while (per < most && per < range) per *= 2;
+  FewPlan plan(rows, per, range, p.bits, p.group, p.m, !one);
+  while (plan.smem > 72 * 1024 && per > 1) {
+    per /= 2;
+    plan = FewPlan(rows, per, range, p.bits, p.group, p.m, !one);
+  }
+  plan.blocks = blocks;
+  plan.rank_shift = shift;
+  const void* kern = one         ? few_kernel<X, 1, 1>(p.bits)
+                     : p.m <= 8  ? few_kernel<X, 1, 4>(p.bits)
+                     : p.m <= 16 ? few_kernel<X, 2, 4>(p.bits)
+                                 : few_kernel<X, 4, 4>(p.bits);
+  CK(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, plan.smem));
+  const int grid = one && blocks > 3 * num_sms() ? 3 * num_sms() : blocks;
   cudaLaunchConfig_t lc = {};
-  lc.gridDim = dim3((unsigned)(blocks * ranks));
+  lc.gridDim = dim3((unsigned)(grid * ranks));
   lc.blockDim = dim3(kFewThreads);
+  lc.dynamicSmemBytes = plan.smem;
   lc.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -67,10 +82,8 @@ int launch_few(const PackedArgs& p, cudaStream_t st) {
   attr[0].val.clusterDim.z = 1;
   lc.attrs = attr;
   lc.numAttrs = 1;
+  void* argv[] = {&p, &plan};
   count_launch();
-  const void* kern = few_kernel<X>(p.m, p.bits);
-  PackedArgs args = p;
-  void* argv[] = {&args};
   CK(cudaLaunchKernelExC(&lc, kern, argv));
   return ADMMQ_OK;
 }

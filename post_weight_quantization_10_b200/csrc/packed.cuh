@@ -30,28 +30,6 @@ __device__ __forceinline__ void put_out(const PackedArgs& p, long long i, float 
     ((__half*)p.out)[i] = __float2half_rn(v);
 }
 
-// The b words of 32 codes; vec: they start on b words' natural alignment (16
-// bytes for 4 and 8 bits, 8 for 2 and 6).
-template <int B>
-__device__ __forceinline__ void load_words(const uint32_t* p, bool vec, uint32_t (&w)[B]) {
-  if (B % 4 == 0 && vec) {
-#pragma unroll
-    for (int i = 0; i < B / 4; ++i) {
-      const uint4 v = __ldg(reinterpret_cast<const uint4*>(p) + i);
-      w[4 * i] = v.x; w[4 * i + 1] = v.y; w[4 * i + 2] = v.z; w[4 * i + 3] = v.w;
-    }
-  } else if (B % 2 == 0 && vec) {
-#pragma unroll
-    for (int i = 0; i < B / 2; ++i) {
-      const uint2 v = __ldg(reinterpret_cast<const uint2*>(p) + i);
-      w[2 * i] = v.x; w[2 * i + 1] = v.y;
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < B; ++i) w[i] = __ldg(p + i);
-  }
-}
-
 // Bits [at, at + 32) of the word array (what lies past it reads as zero).
 template <int B>
 __device__ __forceinline__ uint32_t bits_at(const uint32_t (&w)[B], int at) {
@@ -62,46 +40,70 @@ __device__ __forceinline__ uint32_t bits_at(const uint32_t (&w)[B], int at) {
   return __funnelshift_r(lo, hi, s);
 }
 
-// 32 codes minus their zero point, as 16 pairs of X in column order.  A code
-// goes into the low mantissa bits of 128 (bf16) or 1024 (fp16), where one
-// step is 1; subtracting 128 + zero (1024 + zero) is exact.  Eight bits do not
-// fit behind bf16's 128: they go through fp32's 2^23 instead.
+// (a & b) | c
+__device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+  return r;
+}
+
+// 32 codes minus their zero point as 16 pairs of X: pair i holds codes i and
+// i + 16.  (The two are 16 b bits apart, so one window of 16 bits from each
+// half of the block, side by side in a word, gives 16 / b pairs by a mask.)  A
+// masked code at bit p goes into the mantissa of 128 (bf16) or 1024 (fp16),
+// whose last bit is worth 1: 128 + 2^p code.  One multiply-add by 2^-p and
+// -(128 2^-p + zero) leaves code - zero; every value on the way is exact.
+// Eight bits do not fit behind bf16's 128: they go through fp32's 2^23.
 template <typename X, int B>
 __device__ __forceinline__ void decode32(const uint32_t (&w)[B], float zero, uint32_t (&out)[16]) {
-  constexpr bool BF = sizeof(X) == 2 && __is_same(X, __nv_bfloat16);
-  constexpr uint32_t MASK = (1u << B) - 1u;
+  constexpr bool BF = __is_same(X, __nv_bfloat16);
   if constexpr (BF && B == 8) {
     const float zz = 8388608.f + zero;
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      const uint32_t v = w[i >> 1];
-      const float lo = __uint_as_float(__byte_perm(v, 0x4B000000u, 0x7650 + (i & 1 ? 2 : 0))) - zz;
-      const float hi = __uint_as_float(__byte_perm(v, 0x4B000000u, 0x7651 + (i & 1 ? 2 : 0))) - zz;
+      const uint32_t sel = 0x7650u + (i & 3);  // byte i % 4, then the three upper bytes of 2^23
+      const float lo = __uint_as_float(__byte_perm(w[i >> 2], 0x4B000000u, sel)) - zz;
+      const float hi = __uint_as_float(__byte_perm(w[4 + (i >> 2)], 0x4B000000u, sel)) - zz;
       const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
       out[i] = *reinterpret_cast<const uint32_t*>(&h);
     }
   } else {
+    constexpr uint32_t MASK = (1u << B) - 1u;
+    constexpr int MANTISSA = BF ? 7 : 10;
+    constexpr int PER = 16 / B;             // codes of a 16-bit window
+    constexpr int FIT = MANTISSA / B;       // of them, without a shift
     constexpr uint32_t MAGIC = BF ? 0x43004300u : 0x64006400u;
-    X z1;
-    if constexpr (BF)
-      z1 = __float2bfloat16_rn(128.f + zero);
-    else
-      z1 = __float2half_rn(1024.f + zero);
+    constexpr float BASE = BF ? 128.f : 1024.f;
+    X minus[FIT];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      // code 2i at bit 0 and code 2i + 1 at bit 16
-      const uint32_t lo = bits_at<B>(w, 2 * i * B) & MASK;
-      const uint32_t t = (2 * i + 1) * B >= 16 ? bits_at<B>(w, (2 * i + 1) * B - 16)
-                                               : w[0] << (16 - (2 * i + 1) * B);
-      const uint32_t v = lo | (t & (MASK << 16)) | MAGIC;
-      if constexpr (BF) {
-        const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&v),
-                                         __halves2bfloat162(z1, z1));
-        out[i] = *reinterpret_cast<const uint32_t*>(&d);
-      } else {
-        const __half2 d =
-            __hsub2(*reinterpret_cast<const __half2*>(&v), __halves2half2(z1, z1));
-        out[i] = *reinterpret_cast<const uint32_t*>(&d);
+    for (int f = 0; f < FIT; ++f) {
+      const float c = -(BASE / (float)(1 << (f * B)) + zero);
+      if constexpr (BF)
+        minus[f] = __float2bfloat16_rn(c);
+      else
+        minus[f] = __float2half_rn(c);
+    }
+#pragma unroll
+    for (int c0 = 0; c0 < 16; c0 += PER) {
+      const uint32_t t = __byte_perm(bits_at<B>(w, B * c0), bits_at<B>(w, B * (c0 + 16)), 0x5410);
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        if (c0 + i >= 16) break;
+        const int f = i % FIT;
+        const uint32_t m = (MASK | (MASK << 16)) << (f * B);
+        const uint32_t v = and_or(t >> ((i - f) * B), m, MAGIC);
+        if constexpr (BF) {
+          const X up = __float2bfloat16_rn(1.f / (float)(1 << (f * B)));
+          const __nv_bfloat162 d = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&v),
+                                           __halves2bfloat162(up, up),
+                                           __halves2bfloat162(minus[f], minus[f]));
+          out[c0 + i] = *reinterpret_cast<const uint32_t*>(&d);
+        } else {
+          const X up = __float2half_rn(1.f / (float)(1 << (f * B)));
+          const __half2 d = __hfma2(*reinterpret_cast<const __half2*>(&v), __halves2half2(up, up),
+                                    __halves2half2(minus[f], minus[f]));
+          out[c0 + i] = *reinterpret_cast<const uint32_t*>(&d);
+        }
       }
     }
   }

@@ -1,176 +1,355 @@
-// packed_few.cuh -- product of a few tokens (at most 16) with packed b-bit
-// codes.  The weights are read once, straight into the registers that feed
-// the matrix instructions.
+// packed_few.cuh -- product of a few tokens (at most 32) with packed b-bit
+// codes, on mma.sync.  What bounds it is reading the weights once and turning
+// each code into an operand.
 //
 // mma.m16n8k16 sums over k in an order that nothing depends on, so each of the
 // four lanes that share a weight row takes 32 consecutive codes of a
-// 128-column span (b whole words) and the lane that holds the activations of a
-// token reads the same 32 columns.  Eight instructions use up a span.  The
-// codes enter as code - zero, an integer of at most 8 bits and exact in bf16
-// and fp16; a group's sum leaves the tensor core in fp32 and is scaled there.
-// A group of 64 or 32 columns is summed by itself by running the span's
-// instructions once per group with the other groups' activations set to zero:
-// the matrix pipe has room for it, and the decoded codes stay in registers.
+// 128-column span (b whole words), and the lane that holds a token's
+// activations the same 32 columns, in the pairs that decode32 gives.  Eight
+// instructions use up a span of 16 rows.  The codes enter as code - zero, an
+// integer that bf16 and fp16 hold exactly; a group's sum leaves the tensor
+// core in fp32 and is scaled there.  A group of 64 or 32 columns is summed by
+// itself by running the span's instructions once per group with the other
+// groups' activations set to zero.
 #pragma once
+#include "async.cuh"
 #include "packed.cuh"
 #include "ptx.cuh"
 
 namespace admmq {
 
-constexpr int kFewRows = 64;      // output columns (weight rows) of a block
 constexpr int kFewThreads = 256;
 
 template <typename X>
 __device__ __forceinline__ void mma_m16n8k16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                             uint32_t a3, uint32_t b0, uint32_t b1);
-template <>
-__device__ __forceinline__ void mma_m16n8k16<__nv_bfloat16>(float (&d)[4], uint32_t a0, uint32_t a1,
-                                                            uint32_t a2, uint32_t a3, uint32_t b0,
-                                                            uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-      "{%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-template <>
-__device__ __forceinline__ void mma_m16n8k16<__half>(float (&d)[4], uint32_t a0, uint32_t a1,
-                                                     uint32_t a2, uint32_t a3, uint32_t b0,
-                                                     uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-      "{%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-// A block takes 64 output columns and one of the cluster's ranges of spans;
-// its warps take spans in turn.
-template <typename X, int NT, int B>
-__device__ __forceinline__ void packed_few(const PackedArgs& p, float (&acc)[4][NT][4], int block,
-                                           int sp0, int sp1) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int r = lane >> 2, q = lane & 3;
-  const int passes = 128 / p.group;
-  const bool vec = p.words % 4 == 0;  // rows start on 16 bytes
-  for (int sp = sp0 + warp; sp < sp1; sp += kFewThreads / 32) {
-    const int k = sp * 128 + 32 * q;   // this lane's 32 columns
-    const bool in = k < p.k;
-    uint32_t w[8][B];
-    float z[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const long long row = (long long)block * kFewRows + i * 8 + r;
-      if (in && row < p.n) {
-        load_words<B>(p.packed + row * p.words + (sp * 4 + q) * B, vec, w[i]);
-        z[i] = __ldg(p.zero + row * p.groups + k / p.group);
-      } else {
-#pragma unroll
-        for (int j = 0; j < B; ++j) w[i][j] = 0u;
-        z[i] = 0.f;
-      }
-    }
-    uint32_t x[NT][16];
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      const int token = t * 8 + r;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (in && token < p.m)
-          v = __ldg(reinterpret_cast<const uint4*>((const X*)p.x + token * p.ldx + k) + i);
-        x[t][4 * i] = v.x; x[t][4 * i + 1] = v.y; x[t][4 * i + 2] = v.z; x[t][4 * i + 3] = v.w;
-      }
-    }
-#pragma unroll
-    for (int rt = 0; rt < 4; ++rt) {
-      uint32_t a[2][16];
-      decode32<X, B>(w[2 * rt], z[2 * rt], a[0]);
-      decode32<X, B>(w[2 * rt + 1], z[2 * rt + 1], a[1]);
-      const long long row = (long long)block * kFewRows + rt * 16 + r;
-      for (int g = 0; g < passes; ++g) {
-        const int gi = sp * passes + g;
-        const bool mine = passes == 1 || q * passes / 4 == g;
-        const bool there = gi < p.groups;
-        const float s0 = there && row < p.n ? __ldg(p.scale + row * p.groups + gi) : 0.f;
-        const float s1 = there && row + 8 < p.n ? __ldg(p.scale + (row + 8) * p.groups + gi) : 0.f;
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          float d[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            mma_m16n8k16<X>(d, a[0][2 * j], a[1][2 * j], a[0][2 * j + 1], a[1][2 * j + 1],
-                            mine ? x[t][2 * j] : 0u, mine ? x[t][2 * j + 1] : 0u);
-          acc[rt][t][0] += s0 * d[0];
-          acc[rt][t][1] += s0 * d[1];
-          acc[rt][t][2] += s1 * d[2];
-          acc[rt][t][3] += s1 * d[3];
-        }
-      }
-    }
-  }
-}
-
-template <typename X, int NT, int B>
-__global__ void __launch_bounds__(kFewThreads) k_packed_few(const PackedArgs p) {
-  __shared__ float part[kFewThreads / 32][8 * NT][kFewRows];
-  __shared__ float sum[8 * NT][kFewRows];
-  uint32_t rank, ranks;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
-  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(ranks));
-  const int block = blockIdx.x / ranks;
-  const int spans = (p.k + 127) / 128;
-  const int sp0 = (int)((long long)rank * spans / ranks), sp1 = (int)((long long)(rank + 1) * spans / ranks);
-  float acc[4][NT][4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) acc[i][t][j] = 0.f;
-  packed_few<X, NT, B>(p, acc, block, sp0, sp1);
-  // the warps' sums, then the cluster's, each in a fixed order
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-#pragma unroll
-  for (int rt = 0; rt < 4; ++rt)
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        part[warp][t * 8 + 2 * (lane & 3) + (j & 1)][rt * 16 + (lane >> 2) + 8 * (j >> 1)] =
-            acc[rt][t][j];
-  __syncthreads();
-  constexpr int OUT = 8 * NT * kFewRows;
-  for (int i = threadIdx.x; i < OUT; i += kFewThreads) {
-    float v = 0.f;
-#pragma unroll
-    for (int w = 0; w < kFewThreads / 32; ++w) v += part[w][i / kFewRows][i % kFewRows];
-    sum[i / kFewRows][i % kFewRows] = v;
-  }
-  if (ranks > 1)
-    cluster_sync();
+                                             uint32_t a3, uint32_t b0, uint32_t b1) {
+  if constexpr (__is_same(X, __nv_bfloat16))
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
   else
-    __syncthreads();
-  for (int i = rank * kFewThreads + threadIdx.x; i < OUT; i += ranks * kFewThreads) {
-    const int token = i / kFewRows;
-    const long long col = (long long)block * kFewRows + i % kFewRows;
-    if (token >= p.m || col >= p.n) continue;
-    float v = 0.f;
-    if (ranks > 1) {
-      for (uint32_t c = 0; c < ranks; ++c) {
-        float f;
-        asm volatile("ld.shared::cluster.f32 %0, [%1];"
-                     : "=f"(f)
-                     : "r"(cluster_addr(smem_u32(&sum[token][i % kFewRows]), c))
-                     : "memory");
-        v += f;
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Asynchronous copies that write zeros where there is nothing to read.
+__device__ __forceinline__ void cp_async4_or_zero(uint32_t dst, const void* src, bool there) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src),
+               "r"(there ? 4 : 0)
+               : "memory");
+}
+
+// How a block's work is laid out (made on the host).  A stage of the pipeline
+// holds `spans` spans (a power of two) of the block's 16 RT rows: packed rows,
+// scales and zero points ([row][group]).  The activations lie behind the
+// stages, for the whole range or (x_staged) for a stage each, and behind them
+// 64 bytes of zeros that the lanes of tokens that do not exist read.  Rows of
+// words are spaced so that the 32 lanes' words (B (4 row + lane % 4) apart)
+// fall into different banks, tokens 64 bytes off a multiple of 128 for the
+// same reason.
+struct FewPlan {
+  int spans, range;                // per stage; of a rank
+  int blocks;                      // row blocks
+  int rank_shift, passes, groups;  // log2 ranks; groups of a span; of a stage
+  int x_staged;
+  int pitch, x_pitch;              // of a row in words, of a token in bytes
+  int s_off, bytes;                // of a stage
+  int x_off, x_bytes, smem;
+  FewPlan(int rows, int spans_, int range_, int bits, int group, int tokens, bool staged) {
+    spans = spans_;
+    range = range_;
+    x_staged = staged;
+    passes = 128 / group;
+    groups = spans * passes;
+    pitch = spans * 4 * bits;
+    pitch += (4 * bits - pitch) & 31;
+    const int x_spans = staged || spans > range ? spans : range;
+    x_pitch = x_spans * 256 + 64;
+    s_off = rows * pitch * 4;
+    bytes = (s_off + 2 * rows * groups * 4 + 127) & ~127;
+    x_off = 2 * bytes;
+    x_bytes = (tokens * x_pitch + 127) & ~127;
+    smem = x_off + (staged ? 2 : 1) * x_bytes + 64;
+  }
+};
+
+// A block takes 16 RT output columns and one of the cluster's ranges of spans
+// (and, with RT = 1, further row blocks after that), a stage at a time: the
+// next stage's words are on their way while one is used.  Its eight warps are
+// RT row tiles of 16 by 8 / RT shares of the spans.  RT = 1 keeps all of the
+// activations in shared memory, which few tokens allow; with more tokens RT = 4
+// reads them from L2 a quarter as often.
+template <typename X, int NT, int RT, int B>
+__global__ void __launch_bounds__(kFewThreads, 3)
+    k_packed_few(const __grid_constant__ PackedArgs p, const __grid_constant__ FewPlan st) {
+  constexpr int ROWS = 16 * RT, KW = 8 / RT;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ float sum[RT == 1 ? 8 : 1][8 * NT][ROWS];
+  __shared__ uint64_t full[2];
+  __shared__ int abort_flag;
+  const int ranks = 1 << st.rank_shift, rank = blockIdx.x & (ranks - 1);
+  const int block0 = blockIdx.x >> st.rank_shift, block_step = gridDim.x >> st.rank_shift;
+  const int sp0 = rank * st.range, sp1 = min(sp0 + st.range, (p.k + 127) >> 7);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int r = lane >> 2, q = lane & 3, rt = RT == 1 ? 0 : warp & (RT - 1), kw = warp / RT;
+  const int passes = st.passes;
+  const bool vec = (p.words & 3) == 0;  // rows of words start on 16 bytes
+  const bool vec_s = ((p.groups | st.groups) & 3) == 0 &&
+                     (((uintptr_t)p.scale | (uintptr_t)p.zero) & 15) == 0;  // so do their scales
+
+  // Words, scales and zero points of the spans from sp on into a stage.  The
+  // words of a row are one bulk copy (rows that start on 16 bytes; others go
+  // word by word).  What lies behind the last column or row is not read: such
+  // codes meet activations and scales of zero, or outputs that do not exist.
+  auto fetch = [&](int block, int sp, int buf) {
+    const long long row0 = (long long)block * ROWS;
+    const int rows = p.n - row0 < ROWS ? (int)(p.n - row0) : ROWS;
+    const uint32_t base = smem_u32(smem) + buf * st.bytes, bar = smem_u32(&full[buf]);
+    const int first = sp * 4 * B, words = min(min(st.spans, sp1 - sp) * 4 * B, p.words - first);
+    const int g0 = sp * passes, groups = min(st.groups, p.groups - g0);
+    const int t = threadIdx.x;
+    if (t == 0)
+      mbar_arrive_expect_tx(bar, rows * ((vec ? words * 4 : 0) + (vec_s ? groups * 8 : 0)));
+    if (vec) {
+      if (t < rows)
+        bulk_load(base + t * st.pitch * 4, p.packed + (row0 + t) * p.words + first, words * 4, bar);
+    } else {
+      for (int row = warp; row < rows; row += kFewThreads / 32)
+        for (int c = lane; c < words; c += 32)
+          cp_async4_or_zero(base + (row * st.pitch + c) * 4,
+                            p.packed + (row0 + row) * p.words + first + c, true);
+    }
+    const uint32_t s_dst = base + st.s_off, z_dst = s_dst + ROWS * st.groups * 4;
+    if (vec_s) {
+      const int row = t - 64;
+      if (row >= 0 && row < rows)
+        bulk_load(s_dst + row * st.groups * 4, p.scale + (row0 + row) * p.groups + g0, groups * 4, bar);
+      if (row >= 64 && row - 64 < rows)
+        bulk_load(z_dst + (row - 64) * st.groups * 4, p.zero + (row0 + row - 64) * p.groups + g0,
+                  groups * 4, bar);
+    } else {
+      const int shift = __ffs(st.groups) - 1;
+      for (int i = t; i < ROWS << shift; i += kFewThreads) {
+        const int row = i >> shift, c = i & (st.groups - 1);
+        const bool ok = row < rows && c < groups;
+        const long long at = ok ? (row0 + row) * p.groups + g0 + c : 0;
+        cp_async4_or_zero(s_dst + i * 4, p.scale + at, ok);
+        cp_async4_or_zero(z_dst + i * 4, p.zero + at, ok);
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  // Activations of n spans in the order the lanes read them: per token and
+  // span four 16-byte pieces (pairs 4 i .. 4 i + 3) of each of the four lanes.
+  auto fetch_x = [&](int sp, int n, int buf) {
+    uint8_t* base = smem + st.x_off + buf * st.x_bytes;
+    // 8 n half blocks of 16 columns (8 pairs) per token; 8 to 256 threads a token
+    const int shift = n >= 32 ? 8 : 35 - __clz(2 * n - 1 >> 1);
+    for (int token = threadIdx.x >> shift; token < p.m; token += kFewThreads >> shift)
+      for (int c = threadIdx.x & ((1 << shift) - 1); c < 8 * n; c += 1 << shift) {
+        const int block32 = c >> 1, half = c & 1;       // columns 8 half .. + 7 and 16 + 8 half ..
+        const int k = sp * 128 + block32 * 32;
+        uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
+        if (k < p.k) {
+          const X* src = (const X*)p.x + token * p.ldx + k + 8 * half;
+          lo = __ldg(reinterpret_cast<const uint4*>(src));
+          hi = __ldg(reinterpret_cast<const uint4*>(src + 16));
+        }
+        uint4 a, b;
+        a.x = __byte_perm(lo.x, hi.x, 0x5410); a.y = __byte_perm(lo.x, hi.x, 0x7632);
+        a.z = __byte_perm(lo.y, hi.y, 0x5410); a.w = __byte_perm(lo.y, hi.y, 0x7632);
+        b.x = __byte_perm(lo.z, hi.z, 0x5410); b.y = __byte_perm(lo.z, hi.z, 0x7632);
+        b.z = __byte_perm(lo.w, hi.w, 0x5410); b.w = __byte_perm(lo.w, hi.w, 0x7632);
+        uint4* dst = reinterpret_cast<uint4*>(base + token * st.x_pitch + (block32 >> 2) * 256);
+        dst[(2 * half) * 4 + (block32 & 3)] = a;
+        dst[(2 * half + 1) * 4 + (block32 & 3)] = b;
+      }
+  };
+
+  if (threadIdx.x == 0) {
+    mbar_init(smem_u32(&full[0]), 1);
+    mbar_init(smem_u32(&full[1]), 1);
+    abort_flag = 0;
+    fence_barrier_init();
+  }
+  uint8_t* nothing = smem + st.x_off + (st.x_staged ? 2 : 1) * st.x_bytes;
+  if (threadIdx.x < 16) reinterpret_cast<uint32_t*>(nothing)[threadIdx.x] = 0u;
+  __syncthreads();
+  // the items of this block, (row block, stage) in turn: the next one to fetch
+  int f_block = block0, f_sp = sp0;
+  auto fetch_next = [&](int buf) {
+    if (f_block < st.blocks && f_sp < sp1) {
+      fetch(f_block, f_sp, buf);
+      f_sp += st.spans;
+      if (f_sp >= sp1) {
+        f_sp = sp0;
+        f_block += block_step;
       }
     } else {
-      v = sum[token][i % kFewRows];
+      asm volatile("cp.async.commit_group;" ::: "memory");
     }
-    put_out(p, (long long)token * p.n + col, v);
+  };
+  fetch_next(0);
+  fetch_next(1);
+  if (!st.x_staged) fetch_x(sp0, sp1 - sp0, 0);
+  bool ok = true;
+  int buf = 0;
+  uint32_t phase = 0;
+  for (int block = block0; block < st.blocks; block += block_step) {
+    const long long row0 = (long long)block * ROWS;
+    float acc[NT][4];
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[t][j] = 0.f;
+    for (int sp = sp0; sp < sp1; sp += st.spans) {
+      const int there = min(st.spans, sp1 - sp);
+      if (st.x_staged) fetch_x(sp, there, buf);
+      asm volatile("cp.async.wait_group 1;" ::: "memory");
+      ok = mbar_wait(smem_u32(&full[buf]), phase, &abort_flag, nullptr) && ok;
+      __syncthreads();
+      const uint8_t* base = smem + buf * st.bytes;
+      const uint32_t* src =
+          reinterpret_cast<const uint32_t*>(base) + (rt * 16 + r) * st.pitch + (4 * kw + q) * B;
+      const int low = 8 * st.pitch;      // to the lane's second row
+      const float* scales =
+          reinterpret_cast<const float*>(base + st.s_off) + (rt * 16 + r) * st.groups + kw * passes;
+      const float* zeros = scales + ROWS * st.groups + (q * passes >> 2);
+      const int low_s = 8 * st.groups;
+      const uint8_t* xs[NT];
+      int x_step[NT];
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        const bool token = t * 8 + r < p.m;
+        xs[t] = token ? smem + st.x_off + (st.x_staged ? buf * st.x_bytes : (sp - sp0) * 256) +
+                            (t * 8 + r) * st.x_pitch + kw * 256 + q * 16
+                      : nothing;
+        x_step[t] = token ? 64 : 0;
+      }
+      for (int i = kw; i < there; i += KW) {
+        uint32_t w0[B], w1[B], a0[16], a1[16];
+        if constexpr (B % 4 == 0) {
+#pragma unroll
+          for (int j = 0; j < B / 4; ++j) {
+            const uint4 u = reinterpret_cast<const uint4*>(src)[j];
+            const uint4 v = reinterpret_cast<const uint4*>(src + low)[j];
+            w0[4 * j] = u.x; w0[4 * j + 1] = u.y; w0[4 * j + 2] = u.z; w0[4 * j + 3] = u.w;
+            w1[4 * j] = v.x; w1[4 * j + 1] = v.y; w1[4 * j + 2] = v.z; w1[4 * j + 3] = v.w;
+          }
+        } else if constexpr (B % 2 == 0) {
+#pragma unroll
+          for (int j = 0; j < B / 2; ++j) {
+            const uint2 u = reinterpret_cast<const uint2*>(src)[j];
+            const uint2 v = reinterpret_cast<const uint2*>(src + low)[j];
+            w0[2 * j] = u.x; w0[2 * j + 1] = u.y;
+            w1[2 * j] = v.x; w1[2 * j + 1] = v.y;
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < B; ++j) {
+            w0[j] = src[j];
+            w1[j] = src[low + j];
+          }
+        }
+        decode32<X, B>(w0, zeros[0], a0);
+        decode32<X, B>(w1, zeros[low_s], a1);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          uint32_t x[16];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint4 v = *reinterpret_cast<const uint4*>(xs[t] + j * x_step[t]);
+            x[4 * j] = v.x; x[4 * j + 1] = v.y; x[4 * j + 2] = v.z; x[4 * j + 3] = v.w;
+          }
+          xs[t] += 4 * KW * x_step[t];
+          if (passes == 1) {
+            float d[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              mma_m16n8k16<X>(d, a0[2 * j], a1[2 * j], a0[2 * j + 1], a1[2 * j + 1], x[2 * j],
+                              x[2 * j + 1]);
+            const float s0 = scales[0], s1 = scales[low_s];
+            acc[t][0] += s0 * d[0];
+            acc[t][1] += s0 * d[1];
+            acc[t][2] += s1 * d[2];
+            acc[t][3] += s1 * d[3];
+          } else {
+            for (int g = 0; g < passes; ++g) {
+              const bool mine = q * passes >> 2 == g;
+              float d[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+              for (int j = 0; j < 8; ++j)
+                mma_m16n8k16<X>(d, a0[2 * j], a1[2 * j], a0[2 * j + 1], a1[2 * j + 1],
+                                mine ? x[2 * j] : 0u, mine ? x[2 * j + 1] : 0u);
+              // no scale is read for a group behind the last column
+              const bool there_g = (sp + i) * passes + g < p.groups;
+              const float s0 = there_g ? scales[g] : 0.f, s1 = there_g ? scales[low_s + g] : 0.f;
+              acc[t][0] += s0 * d[0];
+              acc[t][1] += s0 * d[1];
+              acc[t][2] += s1 * d[2];
+              acc[t][3] += s1 * d[3];
+            }
+          }
+        }
+        src += 4 * KW * B;
+        scales += KW * passes;
+        zeros += KW * passes;
+      }
+      __syncthreads();
+      fetch_next(buf);
+      buf ^= 1;
+      if (buf == 0) phase ^= 1;
+    }
+    // a wait that gave up leaves no number behind
+    if (!ok)
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[t][j] = __int_as_float(0x7FFFFFFF);
+    // the shares' sums, then the cluster's, each in a fixed order
+    if (RT == 1) {
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          sum[RT == 1 ? kw : 0][t * 8 + 2 * q + (j & 1)][r + 8 * (j >> 1)] = acc[t][j];
+      __syncthreads();
+    } else {
+#pragma unroll
+      for (int share = 0; share < KW; ++share) {
+        if (kw == share) {
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              float& at = sum[0][t * 8 + 2 * q + (j & 1)][rt * 16 + r + 8 * (j >> 1)];
+              at = share ? at + acc[t][j] : acc[t][j];
+            }
+        }
+        __syncthreads();
+      }
+    }
+    if (ranks > 1) cluster_sync();
+    for (int i = rank * kFewThreads + threadIdx.x; i < p.m * ROWS; i += ranks * kFewThreads) {
+      const int token = i / ROWS, c = i % ROWS;
+      if (row0 + c >= p.n) continue;
+      float v = 0.f;
+      if (ranks > 1) {
+        for (int k = 0; k < ranks; ++k)
+          v += ld_cluster_f32(cluster_addr(smem_u32(&sum[0][token][c]), k));
+      } else {
+#pragma unroll
+        for (int w = 0; w < (RT == 1 ? 8 : 1); ++w) v += sum[w][token][c];
+      }
+      put_out(p, (long long)token * p.n + row0 + c, v);
+    }
+    if (ranks > 1) cluster_sync();  // the sums stay until every rank has read them
   }
-  if (ranks > 1) cluster_sync();  // the sums stay until every rank has read them
 }
 
 }  // namespace admmq
