@@ -19,7 +19,8 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libadmmq.so")
 SOURCES = ["admmq.cu", "mx.cu", "packed.cu"]
 HEADERS = ["host.cuh", "async.cuh", "ptx.cuh", "gemm.cuh", "kernels.cuh", "admm_loop.cuh", "gptq.cuh", "mx.cuh",
-           "mx_gemm.cuh", "packed.cuh", "packed_few.cuh", "product.cuh"]
+           "mx_gemm.cuh", "packed.cuh", "packed_few.cuh", "packed_gemm.cuh",
+           "tmem_fair.cuh"]
 INCLUDE = os.path.join(os.path.dirname(HERE), "include", "admmq.h")
 
 

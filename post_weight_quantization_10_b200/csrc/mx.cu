@@ -3,6 +3,7 @@
 #include "host.cuh"
 #include "mx.cuh"
 #include "mx_gemm.cuh"
+#include "tmem_fair.cuh"
 
 using namespace admmq;
 
@@ -186,18 +187,6 @@ bool make_codes_map(CUtensorMap* m, const void* ptr, int k, int64_t rows, int bo
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(ptr), dims, strides, box, estr,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// Shared memory to ask for, so that blocks which fit an SM together never ask
-// for more than its 512 tensor-memory columns: the CTAs of a cluster wait for
-// one another, and one of them that waited for columns held by another cluster
-// could close a circle.  Columns and shared memory (228 KB with 1 KB a block)
-// run out together; the 40 KB keep it off the SMs of the layer solve's engine,
-// whose blocks hold all columns and leave 29 KB.
-int tmem_fair_smem(int bytes, int cols) {
-  const int fair = cols * (228 * 1024 / 512) - 1024;
-  if (bytes < fair) bytes = fair;
-  return bytes < 40 * 1024 ? 40 * 1024 : bytes;
 }
 
 template <int FMT, typename T>

@@ -2,35 +2,12 @@
 // layer: out[m][n] = sum over groups G of s[n][G] sum_{k in G} (c[n][k] - z[n][G]) x[m][k].
 #include "host.cuh"
 #include "packed_few.cuh"
-#include "product.cuh"
+#include "packed_gemm.cuh"
+#include "tmem_fair.cuh"
 
 using namespace admmq;
 
 namespace {
-
-template <typename T>
-struct DenseElement {
-  const T* x;
-  long long ld;
-  __device__ __forceinline__ float operator()(long long row, int k) const {
-    return (float)x[row * ld + k];
-  }
-};
-
-struct PackedElement {
-  const uint32_t* packed;
-  const float *scale, *zero;
-  int words, bits, group, groups;
-  __device__ __forceinline__ float operator()(long long row, int k) const {
-    const int pos = k * bits, w = pos >> 5, sh = pos & 31;
-    const uint32_t* p = packed + row * words;
-    uint32_t c = p[w] >> sh;
-    if (sh + bits > 32) c |= p[w + 1] << (32 - sh);
-    c &= (1u << bits) - 1u;
-    const long long g = row * groups + k / group;
-    return ((float)c - zero[g]) * scale[g];
-  }
-};
 
 // Tokens that the mma.sync kernel takes.
 constexpr int kFewTokens = 32;
@@ -88,6 +65,87 @@ int launch_few(PackedArgs p, cudaStream_t st) {
   return ADMMQ_OK;
 }
 
+bool make_x_map(CUtensorMap* m, const PackedArgs& p, bool bf16, int box_rows) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[2] = {(cuuint64_t)p.k, (cuuint64_t)p.m};
+  cuuint64_t strides[1] = {(cuuint64_t)p.ldx * 2};
+  cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
+  cuuint32_t estr[2] = {1, 1};
+  return fn(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
+            const_cast<void*>(p.x), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Packed rows as bytes, boxes of a 128-code chunk (16 b bytes) x 128 rows.
+bool make_w_map(CUtensorMap* m, const PackedArgs& p) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[2] = {(cuuint64_t)p.words * 4, (cuuint64_t)p.n};
+  cuuint64_t strides[1] = {(cuuint64_t)p.words * 4};
+  cuuint32_t box[2] = {(cuuint32_t)(16 * p.bits), 128};
+  cuuint32_t estr[2] = {1, 1};
+  const CUtensorMapSwizzle sw = p.bits == 2   ? CU_TENSOR_MAP_SWIZZLE_32B
+                                : p.bits == 4 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                : p.bits == 8 ? CU_TENSOR_MAP_SWIZZLE_128B
+                                              : CU_TENSOR_MAP_SWIZZLE_NONE;
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint32_t*>(p.packed), dims, strides,
+            box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename X, int TN>
+int launch_gemm_tn(const PackedArgs& p, cudaStream_t st) {
+  using Cfg = PackedCfg<TN>;
+  PackedGemmArgs a;
+  a.p = p;
+  a.tiles_n = cdiv(p.n, 128);
+  const long long tiles = (long long)a.tiles_n * cdiv(p.m, TN);
+  if (tiles > (1 << 28)) return ADMMQ_ERR_UNSUPPORTED;
+  a.tiles = (int)tiles;
+  a.chunks = cdiv(p.k, 128);
+  a.passes = 128 / p.group;
+  a.w_tma = p.words % 4 == 0;
+  int ranks = 1;
+  while (ranks < 8 && a.chunks >= 4 * ranks && tiles * 2 * ranks <= num_sms()) ranks *= 2;
+  a.range = cdiv(a.chunks, ranks);
+  const int room = 226 * 1024, wbytes = 2048 * p.bits;
+  a.stages = 4;
+  a.wbufs = (room - 1024 - a.stages * Cfg::STAGE - 512) / wbytes;
+  if (a.wbufs > 4) a.wbufs = 4;
+  if (!make_x_map(&a.x, p, __is_same(X, __nv_bfloat16), TN)) return ADMMQ_ERR_CUDA;
+  if (a.w_tma && !make_w_map(&a.w, p)) return ADMMQ_ERR_CUDA;
+  int smem = a.stages * Cfg::STAGE + a.wbufs * wbytes + 1024 + 512;
+  smem = tmem_fair_smem(smem, Cfg::TMEM_COLS);
+  auto kern = k_packed_gemm<X, TN>;
+  CK(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+  const long long grid = ranks > 1 ? tiles * ranks : (tiles < num_sms() ? tiles : num_sms());
+  cudaLaunchConfig_t lc = {};
+  lc.gridDim = dim3((unsigned)grid);
+  lc.blockDim = dim3(kPackedThreads);
+  lc.dynamicSmemBytes = smem;
+  lc.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = ranks;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  lc.attrs = attr;
+  lc.numAttrs = 1;
+  count_launch();
+  CK(cudaLaunchKernelEx(&lc, kern, a));
+  return ADMMQ_OK;
+}
+
+template <typename X>
+int launch_packed(const PackedArgs& p, cudaStream_t st) {
+  if (p.m <= kFewTokens) return launch_few<X>(p, st);
+  if (p.m <= 64) return launch_gemm_tn<X, 64>(p, st);
+  if (p.m <= 128) return launch_gemm_tn<X, 128>(p, st);
+  return launch_gemm_tn<X, 256>(p, st);
+}
+
 }  // namespace
 
 extern "C" int admmq_packed_matmul(const void* x, int x_dtype, int64_t m, int64_t ldx,
@@ -105,31 +163,8 @@ extern "C" int admmq_packed_matmul(const void* x, int x_dtype, int64_t m, int64_
     return ADMMQ_ERR_INVALID_ARG;
   int rc = device_ok();
   if (rc) return rc;
-  const PackedElement w{packed, scale, zero, d_in / 32 * bits, bits, group, d_in / group};
-  cudaStream_t st = (cudaStream_t)stream;
-  if (m <= kFewTokens) {
-    const PackedArgs p{x,        packed, scale, zero, out,       ldx, (int)m,
-                       d_out,    d_in,   bits,  group, d_in / 32 * bits, d_in / group, out_dtype};
-    return x_dtype == ADMMQ_DTYPE_BF16 ? launch_few<__nv_bfloat16>(p, st) : launch_few<__half>(p, st);
-  }
-#define PACKED_T(X, T)                                                                          \
-  launch_product<T>(DenseElement<X>{(const X*)x, ldx}, w, (int)m, d_out, d_in, nullptr, nullptr, \
-                    (T*)out, st)
-#define PACKED_X(X)                         \
-  if (out_dtype == ADMMQ_DTYPE_F32) {       \
-    PACKED_T(X, float);                     \
-  } else if (out_dtype == ADMMQ_DTYPE_BF16) { \
-    PACKED_T(X, __nv_bfloat16);             \
-  } else {                                  \
-    PACKED_T(X, __half);                    \
-  }
-  if (x_dtype == ADMMQ_DTYPE_BF16) {
-    PACKED_X(__nv_bfloat16)
-  } else {
-    PACKED_X(__half)
-  }
-#undef PACKED_X
-#undef PACKED_T
-  CK(cudaGetLastError());
-  return ADMMQ_OK;
+  const PackedArgs p{x,     packed, scale, zero,  out,               ldx,           (int)m,
+                     d_out, d_in,   bits,  group, d_in / 32 * bits, d_in / group, out_dtype};
+  return x_dtype == ADMMQ_DTYPE_BF16 ? launch_packed<__nv_bfloat16>(p, (cudaStream_t)stream)
+                                     : launch_packed<__half>(p, (cudaStream_t)stream);
 }

@@ -85,7 +85,7 @@ struct FewPlan {
 // activations in shared memory, which few tokens allow; with more tokens RT = 4
 // reads them from L2 a quarter as often.
 template <typename X, int NT, int RT, int B>
-__global__ void __launch_bounds__(kFewThreads, 3)
+__global__ void __launch_bounds__(kFewThreads, NT == 4 ? 2 : 3)
     k_packed_few(const __grid_constant__ PackedArgs p, const __grid_constant__ FewPlan st) {
   constexpr int ROWS = 16 * RT, KW = 8 / RT;
   extern __shared__ __align__(128) uint8_t smem[];

@@ -1,0 +1,381 @@
+// packed_gemm.cuh -- product of many tokens with packed b-bit codes on the
+// tensor cores:
+//   out[i][j] = sum over groups G of s[j][G] sum_{k in G} (c[j][k] - z[j][G]) x[i][k].
+//
+// The weights are the MMA's first operand: 128 output columns j on the 128
+// tensor-memory lanes, up to 256 tokens along the accumulator's columns.  Four
+// warps turn codes into bf16 or fp16 integers c - z (exact) in the swizzled
+// shared-memory tile that the MMA reads.  Each group is accumulated by itself
+// in one of two tensor-memory slots, and eight warps add s times a finished
+// group to fp32 registers while the next group's MMAs run: the scales never
+// touch a 16-bit number, and the tensor core's own accumulator, which rounds
+// to one side, never sums more than a group.
+#pragma once
+#include "async.cuh"
+#include "packed.cuh"
+#include "ptx.cuh"
+
+namespace admmq {
+
+struct PackedGemmArgs {
+  CUtensorMap x, w;    // activations [m][k]; packed rows in bytes
+  PackedArgs p;
+  int tiles_n, tiles;  // 128-column tiles; all tiles
+  int chunks, range;   // 128-column chunks of k; of them, a rank's
+  int w_tma;           // rows of packed words start on 16 bytes: TMA brings them
+  int stages, wbufs;   // ring depths: operand stages (64 of k), packed chunks
+  int passes;          // groups of a chunk
+};
+
+constexpr int kPackedThreads = 512;
+
+// Thread roles, four warpgroups:
+//   0  warp 0: TMA producer, warp 1: MMA issuer
+//   1  decoders
+//   2, 3  consumers: thread = accumulator row, half of the tile's tokens each
+// One output tile of 128 x TN per cluster and turn; a cluster's CTAs share the
+// reduction (contiguous ranges of chunks) and add their tiles in rank order
+// through distributed shared memory.  A cluster of one goes on to further tiles.
+template <int TN>
+struct PackedCfg {
+  static constexpr int HALF = TN / 2;
+  static constexpr int X_BYTES = TN * 128, A_BYTES = 128 * 128, STAGE = X_BYTES + A_BYTES;
+  static constexpr int TMEM_COLS = 2 * TN;
+};
+
+// Words of unit q (32 codes) of a row of a packed chunk in shared memory.  TMA
+// left rows of 16 B bytes, swizzled where their pitch is 32, 64 or 128 bytes:
+// the eight rows that a phase of the warp reads then lie in different banks.
+template <int B>
+__device__ __forceinline__ void chunk_words(const uint8_t* buf, int row, int q, uint32_t (&w)[B]) {
+  const uint8_t* at = buf + row * (16 * B);
+  if constexpr (B == 8) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const uint4 v = *reinterpret_cast<const uint4*>(at + (((2 * q + j) ^ (row & 7)) << 4));
+      w[4 * j] = v.x; w[4 * j + 1] = v.y; w[4 * j + 2] = v.z; w[4 * j + 3] = v.w;
+    }
+  } else if constexpr (B == 4) {
+    const uint4 v = *reinterpret_cast<const uint4*>(at + ((q ^ ((row >> 1) & 3)) << 4));
+    w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
+  } else if constexpr (B == 2) {
+    const uint2 v =
+        *reinterpret_cast<const uint2*>(at + (((q >> 1) ^ ((row >> 2) & 1)) << 4) + 8 * (q & 1));
+    w[0] = v.x; w[1] = v.y;
+  } else if constexpr (B == 6) {
+#pragma unroll
+    for (int j = 0; j < 3; ++j) {
+      const uint2 v = reinterpret_cast<const uint2*>(at + 24 * q)[j];
+      w[2 * j] = v.x; w[2 * j + 1] = v.y;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < B; ++j) w[j] = reinterpret_cast<const uint32_t*>(at + 4 * B * q)[j];
+  }
+}
+
+// One chunk (128 rows x 128 columns) by the four decoder warps into the
+// operand tiles of its two stages.
+template <typename X, int B>
+__device__ __forceinline__ void decode_chunk(const PackedGemmArgs& a, const uint8_t* buf,
+                                             uint8_t* tile0, uint8_t* tile1, long long row0,
+                                             int chunk, const float (&zero)[4]) {
+  const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3;
+  const int q = lane >> 3;
+  uint8_t* tile = q < 2 ? tile0 : tile1;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int row = warp * 32 + i * 8 + (lane & 7);
+    uint32_t w[B], v[16];
+    if (a.w_tma) {
+      chunk_words<B>(buf, row, q, w);
+    } else {
+      const bool in = row0 + row < a.p.n && chunk * 128 + 32 * q < a.p.k;
+      const uint32_t* src = a.p.packed + (row0 + row) * a.p.words + (chunk * 4 + q) * B;
+#pragma unroll
+      for (int j = 0; j < B; ++j) w[j] = in ? __ldg(src + j) : 0u;
+    }
+    decode32<X, B>(w, zero[i], v);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      // columns 8 c .. 8 c + 7 of the unit, in order again
+      const int h = 4 * (c & 1);
+      const uint32_t sel = c < 2 ? 0x5410 : 0x7632;
+      uint4 o;
+      o.x = __byte_perm(v[2 * h], v[2 * h + 1], sel);
+      o.y = __byte_perm(v[2 * h + 2], v[2 * h + 3], sel);
+      o.z = __byte_perm(v[2 * h + 4], v[2 * h + 5], sel);
+      o.w = __byte_perm(v[2 * h + 6], v[2 * h + 7], sel);
+      *reinterpret_cast<uint4*>(tile + row * 128 + ((((q & 1) * 4 + c) ^ (row & 7)) << 4)) = o;
+    }
+  }
+}
+
+template <typename X, int TN>
+__global__ void __launch_bounds__(kPackedThreads, 1)
+    k_packed_gemm(const __grid_constant__ PackedGemmArgs a) {
+  using Cfg = PackedCfg<TN>;
+  const PackedArgs& p = a.p;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  const int S = a.stages, NW = a.wbufs, wbytes = 2048 * p.bits;
+  uint8_t* wring = smem + S * Cfg::STAGE;
+  uint64_t* full_x = reinterpret_cast<uint64_t*>(wring + NW * wbytes);
+  uint64_t* full_a = full_x + S;
+  uint64_t* empty = full_a + S;
+  uint64_t* wfull = empty + S;
+  uint64_t* wempty = wfull + NW;
+  uint64_t* rfull = wempty + NW;
+  uint64_t* rempty = rfull + 2;
+  uint64_t* drain = rempty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint32_t rank, ranks;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(ranks));
+  const int tile0 = blockIdx.x / ranks, tile_step = gridDim.x / ranks;
+  const int ch0 = rank * a.range, ch1 = min(ch0 + a.range, a.chunks);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(smem_u32(&full_x[s]), 1);
+      mbar_init(smem_u32(&full_a[s]), 128);
+      mbar_init(smem_u32(&empty[s]), 1);
+    }
+    for (int i = 0; i < NW; ++i) {
+      mbar_init(smem_u32(&wfull[i]), 1);
+      mbar_init(smem_u32(&wempty[i]), 128);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&rfull[i]), 1);
+      mbar_init(smem_u32(&rempty[i]), 8);
+    }
+    mbar_init(smem_u32(drain), 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) tmem_alloc(smem_u32(tmem_slot), Cfg::TMEM_COLS);
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const int wg = warp >> 2;
+
+  if (wg == 0) {
+    if constexpr (TN == 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+    if (warp == 0 && lane == 0) {
+      // ---------------------------------------------------------- producer
+      bool ok = true;
+      int it = 0, wi = 0;
+      for (int tile = tile0; tile < a.tiles && ok; tile += tile_step) {
+        const int tn = tile % a.tiles_n, tm = tile / a.tiles_n;
+        for (int ch = ch0; ch < ch1 && ok; ++ch, ++wi) {
+          if (a.w_tma) {
+            const int b = wi % NW;
+            if (wi >= NW &&
+                !mbar_wait(smem_u32(&wempty[b]), (uint32_t)(wi / NW - 1) & 1u, abort_flag, nullptr)) {
+              ok = false;
+              break;
+            }
+            mbar_arrive_expect_tx(smem_u32(&wfull[b]), wbytes);
+            tma_load_2d(smem_u32(wring + b * wbytes), &a.w, ch * 16 * p.bits, tn * 128,
+                        smem_u32(&wfull[b]));
+          }
+          for (int h = 0; h < 2; ++h, ++it) {
+            const int s = it % S;
+            if (it >= S &&
+                !mbar_wait(smem_u32(&empty[s]), (uint32_t)(it / S - 1) & 1u, abort_flag, nullptr)) {
+              ok = false;
+              break;
+            }
+            mbar_arrive_expect_tx(smem_u32(&full_x[s]), Cfg::X_BYTES);
+            tma_load_2d(smem_u32(smem + s * Cfg::STAGE), &a.x, ch * 128 + 64 * h, tm * TN,
+                        smem_u32(&full_x[s]));
+          }
+        }
+      }
+      if (!ok) {
+        // the copies in flight land before the block retires
+        for (int j = max(0, it - S); j < it; ++j)
+          mbar_wait_drain(smem_u32(&full_x[j % S]), (uint32_t)(j / S) & 1u);
+        if (a.w_tma)
+          for (int j = max(0, wi - NW); j < wi; ++j)
+            mbar_wait_drain(smem_u32(&wfull[j % NW]), (uint32_t)(j / NW) & 1u);
+      }
+    } else if (warp == 1 && lane == 0) {
+      // -------------------------------------------------------- MMA issuer
+      constexpr uint32_t IDESC = idesc_f32acc(__is_same(X, __nv_bfloat16) ? 1 : 0, 128, TN, false, false);
+      bool ok = true;
+      int it = 0;
+      uint32_t q = 0;  // groups issued
+      const int per = 128 / a.passes / 16;  // MMAs of a group
+      for (int tile = tile0; tile < a.tiles && ok; tile += tile_step) {
+        for (int ch = ch0; ch < ch1 && ok; ++ch, it += 2) {
+          const int steps = min(8, (p.k - ch * 128) >> 4);  // K = 16 each
+          for (int j = 0; j < 8; ++j) {
+            const int s = (it + (j >> 2)) % S;
+            if ((j & 3) == 0) {
+              const uint32_t ph = (uint32_t)((it + (j >> 2)) / S) & 1u;
+              if (!mbar_wait(smem_u32(&full_a[s]), ph, abort_flag, nullptr) ||
+                  !mbar_wait(smem_u32(&full_x[s]), ph, abort_flag, nullptr)) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+            }
+            if (j < steps) {
+              const uint32_t slot = q & 1u;
+              const bool first = j % per == 0;
+              if (first && q >= 2 &&
+                  !mbar_wait(smem_u32(&rempty[slot]), (q / 2 - 1u) & 1u, abort_flag, nullptr)) {
+                ok = false;
+                break;
+              }
+              if (first) tc_fence_after();
+              const uint32_t st = smem_u32(smem + s * Cfg::STAGE);
+              mma_f16(tmem + slot * TN, smem_desc_sw128(st + Cfg::X_BYTES, 16, 1024) + 2 * (j & 3),
+                      smem_desc_sw128(st, 16, 1024) + 2 * (j & 3), IDESC, first ? 0u : 1u);
+              if (j % per == per - 1) {
+                mma_commit(smem_u32(&rfull[slot]));
+                ++q;
+              }
+            }
+            if ((j & 3) == 3) mma_commit(smem_u32(&empty[s]));
+          }
+        }
+      }
+      mma_commit(smem_u32(drain));
+      mbar_wait_drain(smem_u32(drain), 0);
+    }
+  } else if (wg == 1) {
+    // -------------------------------------------------------------- decoders
+    if constexpr (TN == 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    bool ok = true;
+    int it = 0, wi = 0;
+    const int q = lane >> 3;
+    for (int tile = tile0; tile < a.tiles && ok; tile += tile_step) {
+      const long long row0 = (long long)(tile % a.tiles_n) * 128;
+      float next[4], zero[4];
+      auto load_zeros = [&](int ch) {
+        const int k = ch * 128 + 32 * q;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const long long row = row0 + (warp & 3) * 32 + i * 8 + (lane & 7);
+          next[i] = row < p.n && k < p.k ? __ldg(p.zero + row * p.groups + k / p.group) : 0.f;
+        }
+      };
+      load_zeros(ch0);
+      for (int ch = ch0; ch < ch1; ++ch, ++wi, it += 2) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) zero[i] = next[i];
+        if (ch + 1 < ch1) load_zeros(ch + 1);
+        const int b = wi % NW, s0 = it % S, s1 = (it + 1) % S;
+        if (a.w_tma) ok = mbar_wait(smem_u32(&wfull[b]), (uint32_t)(wi / NW) & 1u, abort_flag, nullptr);
+        if (ok && it >= S)
+          ok = mbar_wait(smem_u32(&empty[s0]), (uint32_t)(it / S - 1) & 1u, abort_flag, nullptr);
+        if (ok && it + 1 >= S)
+          ok = mbar_wait(smem_u32(&empty[s1]), (uint32_t)((it + 1) / S - 1) & 1u, abort_flag, nullptr);
+        if (!ok) break;
+        const uint8_t* buf = wring + b * wbytes;
+        uint8_t* t0 = smem + s0 * Cfg::STAGE + Cfg::X_BYTES;
+        uint8_t* t1 = smem + s1 * Cfg::STAGE + Cfg::X_BYTES;
+        switch (p.bits) {
+          case 1: decode_chunk<X, 1>(a, buf, t0, t1, row0, ch, zero); break;
+          case 2: decode_chunk<X, 2>(a, buf, t0, t1, row0, ch, zero); break;
+          case 3: decode_chunk<X, 3>(a, buf, t0, t1, row0, ch, zero); break;
+          case 4: decode_chunk<X, 4>(a, buf, t0, t1, row0, ch, zero); break;
+          case 5: decode_chunk<X, 5>(a, buf, t0, t1, row0, ch, zero); break;
+          case 6: decode_chunk<X, 6>(a, buf, t0, t1, row0, ch, zero); break;
+          case 7: decode_chunk<X, 7>(a, buf, t0, t1, row0, ch, zero); break;
+          default: decode_chunk<X, 8>(a, buf, t0, t1, row0, ch, zero); break;
+        }
+        // the MMA reads what these stores wrote through the async proxy
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        mbar_arrive(smem_u32(&full_a[s0]));
+        mbar_arrive(smem_u32(&full_a[s1]));
+        if (a.w_tma) mbar_arrive(smem_u32(&wempty[b]));
+      }
+    }
+  } else {
+    // ------------------------------------------------------------- consumers
+    if constexpr (TN == 256) asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+    constexpr int HALF = Cfg::HALF;
+    const int half = wg - 2;
+    const int row = (warp & 3) * 32 + lane;
+    const uint32_t ta = tmem + ((uint32_t)((warp & 3) * 32) << 16) + half * HALF;
+    bool ok = true;
+    uint32_t q = 0;
+    for (int tile = tile0; tile < a.tiles; tile += tile_step) {
+      const int tm = tile / a.tiles_n;
+      const long long col = (long long)(tile % a.tiles_n) * 128 + row;
+      float acc[HALF];
+#pragma unroll
+      for (int i = 0; i < HALF; ++i) acc[i] = 0.f;
+      const int g0 = ch0 * a.passes, g1 = min(ch1 * a.passes, p.groups);
+      const float* scale = p.scale + col * p.groups;
+      float s = col < p.n && g0 < g1 ? __ldg(scale + g0) : 0.f;
+      for (int g = g0; g < g1; ++g, ++q) {
+        const float here = s;
+        if (g + 1 < g1) s = col < p.n ? __ldg(scale + g + 1) : 0.f;
+        const uint32_t slot = q & 1u;
+        if (ok) {
+          ok = mbar_wait(smem_u32(&rfull[slot]), (q / 2) & 1u, abort_flag, nullptr);
+          ok = __all_sync(~0u, ok);
+        }
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll
+        for (int j = 0; j < HALF / 16; ++j) {
+          float v[16];
+          tmem_ld16(ta + slot * TN + 16 * j, v);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) acc[16 * j + i] += here * v[i];
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&rempty[slot]));
+      }
+      if (!ok)
+#pragma unroll
+        for (int i = 0; i < HALF; ++i) acc[i] = __int_as_float(0x7FFFFFFF);
+      if (ranks == 1) {
+        const int token0 = tm * TN + half * HALF;
+        if (col < p.n) {
+#pragma unroll
+          for (int i = 0; i < HALF; ++i)
+            if (token0 + i < p.m) put_out(p, (long long)(token0 + i) * p.n + col, acc[i]);
+        }
+      } else {
+        float* part = reinterpret_cast<float*>(smem);  // [TN][128], over the used stages
+#pragma unroll
+        for (int i = 0; i < HALF; ++i) part[(half * HALF + i) * 128 + row] = acc[i];
+      }
+    }
+  }
+  if (ranks > 1) {
+    __syncwarp();
+    cluster_sync();
+    const int row = threadIdx.x & 127;
+    const long long col = (long long)(tile0 % a.tiles_n) * 128 + row;
+    const int token0 = tile0 / a.tiles_n * TN;
+    const float* part = reinterpret_cast<const float*>(smem);
+    if (col < p.n)
+      for (int c = rank + ranks * (threadIdx.x >> 7); c < TN && token0 + c < p.m;
+           c += ranks * (kPackedThreads / 128)) {
+        float v = 0.f;
+        for (uint32_t r = 0; r < ranks; ++r)
+          v += ld_cluster_f32(cluster_addr(smem_u32(part + c * 128 + row), r));
+        put_out(p, (long long)(token0 + c) * p.n + col, v);
+      }
+    cluster_sync();
+  }
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, Cfg::TMEM_COLS);
+  }
+}
+
+}  // namespace admmq

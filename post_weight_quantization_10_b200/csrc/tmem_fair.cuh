@@ -1,0 +1,19 @@
+// tmem_fair.cuh -- how much shared memory a kernel that allocates tensor
+// memory asks for.
+#pragma once
+
+namespace admmq {
+
+// Shared memory to ask for, so that blocks which fit an SM together never ask
+// for more than its 512 tensor-memory columns: the CTAs of a cluster wait for
+// one another, and one of them that waited for columns held by another cluster
+// could close a circle.  Columns and shared memory (228 KB with 1 KB a block)
+// run out together; the 40 KB keep it off the SMs of the layer solve's engine,
+// whose blocks hold all columns and leave 29 KB.
+inline int tmem_fair_smem(int bytes, int cols) {
+  const int fair = cols * (228 * 1024 / 512) - 1024;
+  if (bytes < fair) bytes = fair;
+  return bytes < 40 * 1024 ? 40 * 1024 : bytes;
+}
+
+}  // namespace admmq
