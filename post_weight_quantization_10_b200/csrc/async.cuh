@@ -5,6 +5,20 @@
 
 namespace admmq {
 
+// Position in a ring of n buffers: the buffer and the parity of its use.  (A
+// role is one thread or a few warps: a division per step would be most of its
+// time.)
+struct Ring {
+  int i = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void next(int n) {
+    if (++i == n) {
+      i = 0;
+      phase ^= 1u;
+    }
+  }
+};
+
 // Untiled asynchronous copy global -> shared (16-byte aligned, size a multiple
 // of 16), completing on an mbarrier.
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,

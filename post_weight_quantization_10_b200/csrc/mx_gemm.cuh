@@ -127,57 +127,63 @@ __global__ void __launch_bounds__(kMxTileThreads)
   if (warp == 0) {
     if (lane == 0) {
       bool ok = true;
-      int it = 0;
-      for (int kb = kb0; kb < kb1; ++kb, ++it) {
-        const int s = it % p.stages;
-        if (it >= p.stages &&
-            !mbar_wait(smem_u32(&empty[s]), (uint32_t)(it / p.stages - 1) & 1u, abort_flag, nullptr)) {
+      Ring r;
+      int loads = 0;
+      // a token tile's 128-row scale tiles that exist
+      const int x_row = tm_tile * p.tn >> 7, xrows = min(xt, (p.m + 127) / 128 - x_row);
+      const uint8_t* ws = p.w_scale + ((long long)tn_tile * p.col_tiles + kb0 * NSF) * kScaleTile;
+      const uint8_t* xs = p.x_scale + ((long long)x_row * p.col_tiles + kb0 * NSF) * kScaleTile;
+      for (int kb = kb0; kb < kb1; ++kb, ++loads) {
+        if (!mbar_wait(smem_u32(&empty[r.i]), r.phase ^ 1u, abort_flag, nullptr)) {
           ok = false;
           break;
         }
-        const uint32_t bar = smem_u32(&full[s]), st = smem_u32(smem + s * p.stage_bytes);
+        const uint32_t bar = smem_u32(&full[r.i]), st = smem_u32(smem + r.i * p.stage_bytes);
         const int sf = min(NSF, p.col_tiles - kb * NSF) * kScaleTile;  // scale bytes of this stage
-        // a token tile's 128-row scale tiles that exist
-        const int xrows = min(xt, (p.m + 127) / 128 - (tm_tile * p.tn >> 7));
         mbar_arrive_expect_tx(bar, 128 * 128 + x_bytes + sf * (1 + xrows));
         tma_load_2d(st, &p.w, kb * 128, tn_tile * 128, bar);
         tma_load_2d(st + x_off, &p.x, kb * 128, tm_tile * p.tn, bar);
-        bulk_load(st + sw_off, p.w_scale + ((long long)tn_tile * p.col_tiles + kb * NSF) * kScaleTile,
-                  sf, bar);
+        bulk_load(st + sw_off, ws, sf, bar);
         for (int i = 0; i < xrows; ++i)
-          bulk_load(st + sx_off + i * NSF * kScaleTile,
-                    p.x_scale + (((long long)(tm_tile * p.tn >> 7) + i) * p.col_tiles + kb * NSF) *
-                                    kScaleTile,
+          bulk_load(st + sx_off + i * NSF * kScaleTile, xs + (long long)i * p.col_tiles * kScaleTile,
                     sf, bar);
+        ws += NSF * kScaleTile;
+        xs += NSF * kScaleTile;
+        r.next(p.stages);
       }
       if (!ok)
-        for (int j = max(0, it - p.stages); j < it; ++j)
+        for (int j = max(0, loads - p.stages); j < loads; ++j)
           mbar_wait_drain(smem_u32(&full[j % p.stages]), (uint32_t)(j / p.stages) & 1u);
     }
   } else if (warp == 1) {
     if (lane == 0) {
       const uint32_t sfw = tmem + ((p.tn + 31) & ~31), sfx = sfw + 4 * NSF;
-      for (int kb = kb0, it = 0; kb < kb1; ++kb, ++it) {
-        const int s = it % p.stages;
-        if (!mbar_wait(smem_u32(&full[s]), (uint32_t)(it / p.stages) & 1u, abort_flag, nullptr)) break;
+      Ring r;
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if (!mbar_wait(smem_u32(&full[r.i]), r.phase, abort_flag, nullptr)) break;
         tc_fence_after();
-        const uint32_t st = smem_u32(smem + s * p.stage_bytes);
+        const uint32_t st = smem_u32(smem + r.i * p.stage_bytes);
         const uint64_t dw = smem_desc_sw128(st, 16, 1024), dx = smem_desc_sw128(st + x_off, 16, 1024);
-        const int steps = min(4, (p.k - kb * kMxBK + 63) / 64);
+        const uint64_t dsw = scale_desc(st + sw_off), dsx = scale_desc(st + sx_off);
+        const int steps = min(4, (p.k - kb * kMxBK + 63) >> 6);
         const int tiles = min(NSF, p.col_tiles - kb * NSF);
-        for (int i = 0; i < tiles; ++i) {
-          tmem_copy_scales(sfw + 4 * i, scale_desc(st + sw_off + i * kScaleTile));
+#pragma unroll
+        for (int i = 0; i < NSF; ++i) {
+          if (i >= tiles) break;
+          tmem_copy_scales(sfw + 4 * i, dsw + i * (kScaleTile >> 4));
           for (int j = 0; j < xt; ++j)
-            tmem_copy_scales(sfx + 4 * (i * xt + j),
-                             scale_desc(st + sx_off + (j * NSF + i) * kScaleTile));
+            tmem_copy_scales(sfx + 4 * (i * xt + j), dsx + (j * NSF + i) * (kScaleTile >> 4));
         }
-        for (int j = 0; j < steps; ++j) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (j >= steps) break;
           const int at = FMT == MX_MXFP4 ? j >> 1 : j;
           const uint32_t sf = FMT == MX_MXFP4 ? 2u * (j & 1) : 0u;
           mma_mx<FMT>(tmem, dw + 2 * j, dx + 2 * j, idesc_mx<FMT>(128, p.tn, sf), sfw + 4 * at,
-                      sfx + 4 * at * xt, (it > 0 || j > 0) ? 1u : 0u);
+                      sfx + 4 * at * xt, (kb > kb0 || j > 0) ? 1u : 0u);
         }
-        mma_commit(smem_u32(&empty[s]));
+        mma_commit(smem_u32(&empty[r.i]));
+        r.next(p.stages);
       }
       mma_commit(smem_u32(done));
     }

@@ -100,8 +100,8 @@ int launch_gemm_tn(const PackedArgs& p, cudaStream_t st) {
   using Cfg = PackedCfg<TN>;
   PackedGemmArgs a;
   a.p = p;
-  a.tiles_n = cdiv(p.n, 128);
-  const long long tiles = (long long)a.tiles_n * cdiv(p.m, TN);
+  a.tiles_m = cdiv(p.m, TN);
+  const long long tiles = (long long)a.tiles_m * cdiv(p.n, 128);
   if (tiles > (1 << 28)) return ADMMQ_ERR_UNSUPPORTED;
   a.tiles = (int)tiles;
   a.chunks = cdiv(p.k, 128);

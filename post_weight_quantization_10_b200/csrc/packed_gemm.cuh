@@ -20,7 +20,7 @@ namespace admmq {
 struct PackedGemmArgs {
   CUtensorMap x, w;    // activations [m][k]; packed rows in bytes
   PackedArgs p;
-  int tiles_n, tiles;  // 128-column tiles; all tiles
+  int tiles_m, tiles;  // token tiles; all tiles (token tiles of 128 columns in turn)
   int chunks, range;   // 128-column chunks of k; of them, a rank's
   int w_tma;           // rows of packed words start on 16 bytes: TMA brings them
   int stages, wbufs;   // ring depths: operand stages (64 of k), packed chunks
@@ -142,12 +142,12 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
       mbar_init(smem_u32(&full_x[s]), 1);
-      mbar_init(smem_u32(&full_a[s]), 128);
+      mbar_init(smem_u32(&full_a[s]), 4);
       mbar_init(smem_u32(&empty[s]), 1);
     }
     for (int i = 0; i < NW; ++i) {
       mbar_init(smem_u32(&wfull[i]), 1);
-      mbar_init(smem_u32(&wempty[i]), 128);
+      mbar_init(smem_u32(&wempty[i]), 4);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&rfull[i]), 1);
@@ -168,81 +168,82 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
     if (warp == 0 && lane == 0) {
       // ---------------------------------------------------------- producer
       bool ok = true;
-      int it = 0, wi = 0;
+      Ring x, w;  // a fresh ring's buffers count as emptied once: parity 1
+      int loads = 0, chunks = 0;
       for (int tile = tile0; tile < a.tiles && ok; tile += tile_step) {
-        const int tn = tile % a.tiles_n, tm = tile / a.tiles_n;
-        for (int ch = ch0; ch < ch1 && ok; ++ch, ++wi) {
+        const int tn = tile / a.tiles_m, tm = tile - tn * a.tiles_m;
+        for (int ch = ch0; ch < ch1 && ok; ++ch) {
           if (a.w_tma) {
-            const int b = wi % NW;
-            if (wi >= NW &&
-                !mbar_wait(smem_u32(&wempty[b]), (uint32_t)(wi / NW - 1) & 1u, abort_flag, nullptr)) {
+            const uint32_t bar = smem_u32(&wfull[w.i]);
+            if (!mbar_wait(smem_u32(&wempty[w.i]), w.phase ^ 1u, abort_flag, nullptr)) {
               ok = false;
               break;
             }
-            mbar_arrive_expect_tx(smem_u32(&wfull[b]), wbytes);
-            tma_load_2d(smem_u32(wring + b * wbytes), &a.w, ch * 16 * p.bits, tn * 128,
-                        smem_u32(&wfull[b]));
+            mbar_arrive_expect_tx(bar, wbytes);
+            tma_load_2d(smem_u32(wring + w.i * wbytes), &a.w, ch * 16 * p.bits, tn * 128, bar);
+            w.next(NW);
+            ++chunks;
           }
-          for (int h = 0; h < 2; ++h, ++it) {
-            const int s = it % S;
-            if (it >= S &&
-                !mbar_wait(smem_u32(&empty[s]), (uint32_t)(it / S - 1) & 1u, abort_flag, nullptr)) {
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t bar = smem_u32(&full_x[x.i]);
+            if (!mbar_wait(smem_u32(&empty[x.i]), x.phase ^ 1u, abort_flag, nullptr)) {
               ok = false;
               break;
             }
-            mbar_arrive_expect_tx(smem_u32(&full_x[s]), Cfg::X_BYTES);
-            tma_load_2d(smem_u32(smem + s * Cfg::STAGE), &a.x, ch * 128 + 64 * h, tm * TN,
-                        smem_u32(&full_x[s]));
+            mbar_arrive_expect_tx(bar, Cfg::X_BYTES);
+            tma_load_2d(smem_u32(smem + x.i * Cfg::STAGE), &a.x, ch * 128 + 64 * h, tm * TN, bar);
+            x.next(S);
+            ++loads;
           }
         }
       }
       if (!ok) {
         // the copies in flight land before the block retires
-        for (int j = max(0, it - S); j < it; ++j)
+        for (int j = max(0, loads - S); j < loads; ++j)
           mbar_wait_drain(smem_u32(&full_x[j % S]), (uint32_t)(j / S) & 1u);
-        if (a.w_tma)
-          for (int j = max(0, wi - NW); j < wi; ++j)
-            mbar_wait_drain(smem_u32(&wfull[j % NW]), (uint32_t)(j / NW) & 1u);
+        for (int j = max(0, chunks - NW); j < chunks; ++j)
+          mbar_wait_drain(smem_u32(&wfull[j % NW]), (uint32_t)(j / NW) & 1u);
       }
     } else if (warp == 1 && lane == 0) {
       // -------------------------------------------------------- MMA issuer
       constexpr uint32_t IDESC = idesc_f32acc(__is_same(X, __nv_bfloat16) ? 1 : 0, 128, TN, false, false);
       bool ok = true;
-      int it = 0;
-      uint32_t q = 0;  // groups issued
-      const int per = 128 / a.passes / 16;  // MMAs of a group
+      Ring st, slot;
+      const int last = 128 / a.passes / 16 - 1;  // MMAs of a group (a power of two) - 1
       for (int tile = tile0; tile < a.tiles && ok; tile += tile_step) {
-        for (int ch = ch0; ch < ch1 && ok; ++ch, it += 2) {
+        for (int ch = ch0; ch < ch1 && ok; ++ch) {
           const int steps = min(8, (p.k - ch * 128) >> 4);  // K = 16 each
-          for (int j = 0; j < 8; ++j) {
-            const int s = (it + (j >> 2)) % S;
-            if ((j & 3) == 0) {
-              const uint32_t ph = (uint32_t)((it + (j >> 2)) / S) & 1u;
-              if (!mbar_wait(smem_u32(&full_a[s]), ph, abort_flag, nullptr) ||
-                  !mbar_wait(smem_u32(&full_x[s]), ph, abort_flag, nullptr)) {
-                ok = false;
-                break;
-              }
-              tc_fence_after();
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if (!ok || !mbar_wait(smem_u32(&full_x[st.i]), st.phase, abort_flag, nullptr) ||
+                !mbar_wait(smem_u32(&full_a[st.i]), st.phase, abort_flag, nullptr)) {
+              ok = false;
+              break;
             }
-            if (j < steps) {
-              const uint32_t slot = q & 1u;
-              const bool first = j % per == 0;
-              if (first && q >= 2 &&
-                  !mbar_wait(smem_u32(&rempty[slot]), (q / 2 - 1u) & 1u, abort_flag, nullptr)) {
-                ok = false;
-                break;
+            const uint32_t at = smem_u32(smem + st.i * Cfg::STAGE);
+            const uint64_t dx = smem_desc_sw128(at, 16, 1024);
+            const uint64_t dw = smem_desc_sw128(at + Cfg::X_BYTES, 16, 1024);
+            tc_fence_after();
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const int step = 4 * h + j;
+              if (step >= steps) break;
+              const bool first = (step & last) == 0;
+              if (first) {
+                if (!mbar_wait(smem_u32(&rempty[slot.i]), slot.phase ^ 1u, abort_flag, nullptr)) {
+                  ok = false;
+                  break;
+                }
+                tc_fence_after();
               }
-              if (first) tc_fence_after();
-              const uint32_t st = smem_u32(smem + s * Cfg::STAGE);
-              mma_f16(tmem + slot * TN, smem_desc_sw128(st + Cfg::X_BYTES, 16, 1024) + 2 * (j & 3),
-                      smem_desc_sw128(st, 16, 1024) + 2 * (j & 3), IDESC, first ? 0u : 1u);
-              if (j % per == per - 1) {
-                mma_commit(smem_u32(&rfull[slot]));
-                ++q;
+              mma_f16(tmem + slot.i * TN, dw + 2 * j, dx + 2 * j, IDESC, first ? 0u : 1u);
+              if ((step & last) == last) {
+                mma_commit(smem_u32(&rfull[slot.i]));
+                slot.next(2);
               }
             }
-            if ((j & 3) == 3) mma_commit(smem_u32(&empty[s]));
+            mma_commit(smem_u32(&empty[st.i]));
+            st.next(S);
           }
         }
       }
@@ -253,34 +254,34 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
     // -------------------------------------------------------------- decoders
     if constexpr (TN == 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     bool ok = true;
-    int it = 0, wi = 0;
+    Ring st, wr;
     const int q = lane >> 3;
+    const int group_shift = __ffs(p.group) - 1;
     for (int tile = tile0; tile < a.tiles && ok; tile += tile_step) {
-      const long long row0 = (long long)(tile % a.tiles_n) * 128;
+      const long long row0 = (long long)(tile / a.tiles_m) * 128;
       float next[4], zero[4];
       auto load_zeros = [&](int ch) {
         const int k = ch * 128 + 32 * q;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const long long row = row0 + (warp & 3) * 32 + i * 8 + (lane & 7);
-          next[i] = row < p.n && k < p.k ? __ldg(p.zero + row * p.groups + k / p.group) : 0.f;
+          next[i] = row < p.n && k < p.k ? __ldg(p.zero + row * p.groups + (k >> group_shift)) : 0.f;
         }
       };
       load_zeros(ch0);
-      for (int ch = ch0; ch < ch1; ++ch, ++wi, it += 2) {
+      for (int ch = ch0; ch < ch1; ++ch) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) zero[i] = next[i];
         if (ch + 1 < ch1) load_zeros(ch + 1);
-        const int b = wi % NW, s0 = it % S, s1 = (it + 1) % S;
-        if (a.w_tma) ok = mbar_wait(smem_u32(&wfull[b]), (uint32_t)(wi / NW) & 1u, abort_flag, nullptr);
-        if (ok && it >= S)
-          ok = mbar_wait(smem_u32(&empty[s0]), (uint32_t)(it / S - 1) & 1u, abort_flag, nullptr);
-        if (ok && it + 1 >= S)
-          ok = mbar_wait(smem_u32(&empty[s1]), (uint32_t)((it + 1) / S - 1) & 1u, abort_flag, nullptr);
+        Ring st1 = st;
+        st1.next(S);
+        ok = (!a.w_tma || mbar_wait(smem_u32(&wfull[wr.i]), wr.phase, abort_flag, nullptr)) &&
+             mbar_wait(smem_u32(&empty[st.i]), st.phase ^ 1u, abort_flag, nullptr) &&
+             mbar_wait(smem_u32(&empty[st1.i]), st1.phase ^ 1u, abort_flag, nullptr);
         if (!ok) break;
-        const uint8_t* buf = wring + b * wbytes;
-        uint8_t* t0 = smem + s0 * Cfg::STAGE + Cfg::X_BYTES;
-        uint8_t* t1 = smem + s1 * Cfg::STAGE + Cfg::X_BYTES;
+        const uint8_t* buf = wring + wr.i * wbytes;
+        uint8_t* t0 = smem + st.i * Cfg::STAGE + Cfg::X_BYTES;
+        uint8_t* t1 = smem + st1.i * Cfg::STAGE + Cfg::X_BYTES;
         switch (p.bits) {
           case 1: decode_chunk<X, 1>(a, buf, t0, t1, row0, ch, zero); break;
           case 2: decode_chunk<X, 2>(a, buf, t0, t1, row0, ch, zero); break;
@@ -293,9 +294,15 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
         }
         // the MMA reads what these stores wrote through the async proxy
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        mbar_arrive(smem_u32(&full_a[s0]));
-        mbar_arrive(smem_u32(&full_a[s1]));
-        if (a.w_tma) mbar_arrive(smem_u32(&wempty[b]));
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(smem_u32(&full_a[st.i]));
+          mbar_arrive(smem_u32(&full_a[st1.i]));
+          if (a.w_tma) mbar_arrive(smem_u32(&wempty[wr.i]));
+        }
+        st = st1;
+        st.next(S);
+        wr.next(NW);
       }
     }
   } else {
@@ -306,22 +313,21 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
     const int row = (warp & 3) * 32 + lane;
     const uint32_t ta = tmem + ((uint32_t)((warp & 3) * 32) << 16) + half * HALF;
     bool ok = true;
-    uint32_t q = 0;
+    Ring slot;
     for (int tile = tile0; tile < a.tiles; tile += tile_step) {
-      const int tm = tile / a.tiles_n;
-      const long long col = (long long)(tile % a.tiles_n) * 128 + row;
+      const int tn = tile / a.tiles_m, tm = tile - tn * a.tiles_m;
+      const long long col = (long long)tn * 128 + row;
       float acc[HALF];
 #pragma unroll
       for (int i = 0; i < HALF; ++i) acc[i] = 0.f;
       const int g0 = ch0 * a.passes, g1 = min(ch1 * a.passes, p.groups);
       const float* scale = p.scale + col * p.groups;
       float s = col < p.n && g0 < g1 ? __ldg(scale + g0) : 0.f;
-      for (int g = g0; g < g1; ++g, ++q) {
+      for (int g = g0; g < g1; ++g) {
         const float here = s;
         if (g + 1 < g1) s = col < p.n ? __ldg(scale + g + 1) : 0.f;
-        const uint32_t slot = q & 1u;
         if (ok) {
-          ok = mbar_wait(smem_u32(&rfull[slot]), (q / 2) & 1u, abort_flag, nullptr);
+          ok = mbar_wait(smem_u32(&rfull[slot.i]), slot.phase, abort_flag, nullptr);
           ok = __all_sync(~0u, ok);
         }
         if (!ok) break;
@@ -329,13 +335,14 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
 #pragma unroll
         for (int j = 0; j < HALF / 16; ++j) {
           float v[16];
-          tmem_ld16(ta + slot * TN + 16 * j, v);
+          tmem_ld16(ta + slot.i * TN + 16 * j, v);
 #pragma unroll
           for (int i = 0; i < 16; ++i) acc[16 * j + i] += here * v[i];
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&rempty[slot]));
+        if (lane == 0) mbar_arrive(smem_u32(&rempty[slot.i]));
+        slot.next(2);
       }
       if (!ok)
 #pragma unroll
@@ -358,8 +365,8 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
     __syncwarp();
     cluster_sync();
     const int row = threadIdx.x & 127;
-    const long long col = (long long)(tile0 % a.tiles_n) * 128 + row;
-    const int token0 = tile0 / a.tiles_n * TN;
+    const long long col = (long long)(tile0 / a.tiles_m) * 128 + row;
+    const int token0 = tile0 % a.tiles_m * TN;
     const float* part = reinterpret_cast<const float*>(smem);
     if (col < p.n)
       for (int c = rank + ranks * (threadIdx.x >> 7); c < TN && token0 + c < p.m;
