@@ -19,6 +19,19 @@ struct Ring {
   }
 };
 
+// True for one lane of the (converged) warp.  A role that issues tcgen05
+// instructions runs on its whole warp and elects a lane for the issue alone:
+// descriptors and loop state then stay in uniform registers.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
+
 // Untiled asynchronous copy global -> shared (16-byte aligned, size a multiple
 // of 16), completing on an mbarrier.
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,

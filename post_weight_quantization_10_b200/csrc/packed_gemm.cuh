@@ -111,6 +111,76 @@ __device__ __forceinline__ void decode_chunk(const PackedGemmArgs& a, const uint
   }
 }
 
+// Shared-memory addresses of the barriers (arrays of 8-byte words).
+struct PackedBars {
+  uint32_t full_x, full_a, empty;  // [stages]: activations, decoded weights; stage read
+  uint32_t wfull, wempty;          // [wbufs]: packed chunk there; decoded
+  uint32_t rfull, rempty, drain;   // [2]: group finished; added; everything finished
+  uint32_t end;
+  __device__ PackedBars(uint32_t at, int stages, int wbufs) {
+    full_x = at;
+    full_a = full_x + 8 * stages;
+    empty = full_a + 8 * stages;
+    wfull = empty + 8 * stages;
+    wempty = wfull + 8 * wbufs;
+    rfull = wempty + 8 * wbufs;
+    rempty = rfull + 16;
+    drain = rempty + 16;
+    end = drain + 8;
+  }
+};
+
+// The MMA warp's loop: 8 MMAs of K = 16 per chunk, PASSES groups.
+template <typename X, int TN, int PASSES>
+__device__ __forceinline__ bool issue_mmas(const PackedGemmArgs& a, int ch0, int ch1, int tile0,
+                                           int tile_step, uint32_t tmem, const uint8_t* smem,
+                                           const PackedBars& bars, volatile int* abort_flag) {
+  using Cfg = PackedCfg<TN>;
+  constexpr uint32_t IDESC = idesc_f32acc(__is_same(X, __nv_bfloat16) ? 1 : 0, 128, TN, false, false);
+  constexpr int PER = 8 / PASSES;  // MMAs of a group
+  const uint64_t dx0 = smem_desc_sw128(smem_u32(smem), 16, 1024);
+  const uint64_t dw0 = smem_desc_sw128(smem_u32(smem) + Cfg::X_BYTES, 16, 1024);
+  Ring st, slot;
+  for (int tile = tile0; tile < a.tiles; tile += tile_step) {
+    for (int ch = ch0; ch < ch1; ++ch) {
+      const int groups = min(PASSES, a.p.groups - ch * PASSES);  // of this chunk
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        bool ok = mbar_wait(bars.full_x + 8 * st.i, st.phase, abort_flag, nullptr) &&
+                  mbar_wait(bars.full_a + 8 * st.i, st.phase, abort_flag, nullptr);
+        const uint64_t dx = dx0 + (uint32_t)(st.i * (Cfg::STAGE >> 4));
+        const uint64_t dw = dw0 + (uint32_t)(st.i * (Cfg::STAGE >> 4));
+        // the half's MMAs, a group (or the half of one) at a time
+#pragma unroll
+        for (int j0 = 0; j0 < 4; j0 += PER < 4 ? PER : 4) {
+          const int step = 4 * h + j0;
+          if (step / PER < groups) {
+            if (step % PER == 0)
+              ok = ok && mbar_wait(bars.rempty + 8 * slot.i, slot.phase ^ 1u, abort_flag, nullptr);
+            if (!__all_sync(~0u, ok)) return false;
+            tc_fence_after();
+            const bool ends = (step + (PER < 4 ? PER : 4)) % PER == 0;
+            if (elect_one()) {
+#pragma unroll
+              for (int j = j0; j < j0 + (PER < 4 ? PER : 4); ++j)
+                mma_f16(tmem + slot.i * TN, dw + 2 * j, dx + 2 * j, IDESC,
+                        (4 * h + j) % PER == 0 ? 0u : 1u);
+              if (ends) mma_commit(bars.rfull + 8 * slot.i);
+            }
+            __syncwarp();
+            if (ends) slot.next(2);
+          }
+        }
+        if (!__all_sync(~0u, ok)) return false;
+        if (elect_one()) mma_commit(bars.empty + 8 * st.i);
+        __syncwarp();
+        st.next(a.stages);
+      }
+    }
+  }
+  return true;
+}
+
 template <typename X, int TN>
 __global__ void __launch_bounds__(kPackedThreads, 1)
     k_packed_gemm(const __grid_constant__ PackedGemmArgs a) {
@@ -121,15 +191,8 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
                                              ~static_cast<uintptr_t>(1023));
   const int S = a.stages, NW = a.wbufs, wbytes = 2048 * p.bits;
   uint8_t* wring = smem + S * Cfg::STAGE;
-  uint64_t* full_x = reinterpret_cast<uint64_t*>(wring + NW * wbytes);
-  uint64_t* full_a = full_x + S;
-  uint64_t* empty = full_a + S;
-  uint64_t* wfull = empty + S;
-  uint64_t* wempty = wfull + NW;
-  uint64_t* rfull = wempty + NW;
-  uint64_t* rempty = rfull + 2;
-  uint64_t* drain = rempty + 2;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  const PackedBars bars(smem_u32(wring + NW * wbytes), S, NW);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(wring + NW * wbytes + (bars.end - bars.full_x));
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -141,19 +204,19 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
-      mbar_init(smem_u32(&full_x[s]), 1);
-      mbar_init(smem_u32(&full_a[s]), 4);
-      mbar_init(smem_u32(&empty[s]), 1);
+      mbar_init(bars.full_x + 8 * s, 1);
+      mbar_init(bars.full_a + 8 * s, 4);
+      mbar_init(bars.empty + 8 * s, 1);
     }
     for (int i = 0; i < NW; ++i) {
-      mbar_init(smem_u32(&wfull[i]), 1);
-      mbar_init(smem_u32(&wempty[i]), 4);
+      mbar_init(bars.wfull + 8 * i, 1);
+      mbar_init(bars.wempty + 8 * i, 4);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_u32(&rfull[i]), 1);
-      mbar_init(smem_u32(&rempty[i]), 8);
+      mbar_init(bars.rfull + 8 * i, 1);
+      mbar_init(bars.rempty + 8 * i, 8);
     }
-    mbar_init(smem_u32(drain), 1);
+    mbar_init(bars.drain, 1);
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -174,8 +237,8 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
         const int tn = tile / a.tiles_m, tm = tile - tn * a.tiles_m;
         for (int ch = ch0; ch < ch1 && ok; ++ch) {
           if (a.w_tma) {
-            const uint32_t bar = smem_u32(&wfull[w.i]);
-            if (!mbar_wait(smem_u32(&wempty[w.i]), w.phase ^ 1u, abort_flag, nullptr)) {
+            const uint32_t bar = bars.wfull + 8 * w.i;
+            if (!mbar_wait(bars.wempty + 8 * w.i, w.phase ^ 1u, abort_flag, nullptr)) {
               ok = false;
               break;
             }
@@ -185,8 +248,8 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
             ++chunks;
           }
           for (int h = 0; h < 2; ++h) {
-            const uint32_t bar = smem_u32(&full_x[x.i]);
-            if (!mbar_wait(smem_u32(&empty[x.i]), x.phase ^ 1u, abort_flag, nullptr)) {
+            const uint32_t bar = bars.full_x + 8 * x.i;
+            if (!mbar_wait(bars.empty + 8 * x.i, x.phase ^ 1u, abort_flag, nullptr)) {
               ok = false;
               break;
             }
@@ -200,55 +263,19 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
       if (!ok) {
         // the copies in flight land before the block retires
         for (int j = max(0, loads - S); j < loads; ++j)
-          mbar_wait_drain(smem_u32(&full_x[j % S]), (uint32_t)(j / S) & 1u);
+          mbar_wait_drain(bars.full_x + 8 * (j % S), (uint32_t)(j / S) & 1u);
         for (int j = max(0, chunks - NW); j < chunks; ++j)
-          mbar_wait_drain(smem_u32(&wfull[j % NW]), (uint32_t)(j / NW) & 1u);
+          mbar_wait_drain(bars.wfull + 8 * (j % NW), (uint32_t)(j / NW) & 1u);
       }
-    } else if (warp == 1 && lane == 0) {
+    } else if (warp == 1) {
       // -------------------------------------------------------- MMA issuer
-      constexpr uint32_t IDESC = idesc_f32acc(__is_same(X, __nv_bfloat16) ? 1 : 0, 128, TN, false, false);
-      bool ok = true;
-      Ring st, slot;
-      const int last = 128 / a.passes / 16 - 1;  // MMAs of a group (a power of two) - 1
-      for (int tile = tile0; tile < a.tiles && ok; tile += tile_step) {
-        for (int ch = ch0; ch < ch1 && ok; ++ch) {
-          const int steps = min(8, (p.k - ch * 128) >> 4);  // K = 16 each
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            if (!ok || !mbar_wait(smem_u32(&full_x[st.i]), st.phase, abort_flag, nullptr) ||
-                !mbar_wait(smem_u32(&full_a[st.i]), st.phase, abort_flag, nullptr)) {
-              ok = false;
-              break;
-            }
-            const uint32_t at = smem_u32(smem + st.i * Cfg::STAGE);
-            const uint64_t dx = smem_desc_sw128(at, 16, 1024);
-            const uint64_t dw = smem_desc_sw128(at + Cfg::X_BYTES, 16, 1024);
-            tc_fence_after();
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const int step = 4 * h + j;
-              if (step >= steps) break;
-              const bool first = (step & last) == 0;
-              if (first) {
-                if (!mbar_wait(smem_u32(&rempty[slot.i]), slot.phase ^ 1u, abort_flag, nullptr)) {
-                  ok = false;
-                  break;
-                }
-                tc_fence_after();
-              }
-              mma_f16(tmem + slot.i * TN, dw + 2 * j, dx + 2 * j, IDESC, first ? 0u : 1u);
-              if ((step & last) == last) {
-                mma_commit(smem_u32(&rfull[slot.i]));
-                slot.next(2);
-              }
-            }
-            mma_commit(smem_u32(&empty[st.i]));
-            st.next(S);
-          }
-        }
-      }
-      mma_commit(smem_u32(drain));
-      mbar_wait_drain(smem_u32(drain), 0);
+      const bool ok = a.passes == 1   ? issue_mmas<X, TN, 1>(a, ch0, ch1, tile0, tile_step, tmem, smem, bars, abort_flag)
+                      : a.passes == 2 ? issue_mmas<X, TN, 2>(a, ch0, ch1, tile0, tile_step, tmem, smem, bars, abort_flag)
+                                      : issue_mmas<X, TN, 4>(a, ch0, ch1, tile0, tile_step, tmem, smem, bars, abort_flag);
+      (void)ok;
+      if (elect_one()) mma_commit(bars.drain);
+      __syncwarp();
+      mbar_wait_drain(bars.drain, 0);
     }
   } else if (wg == 1) {
     // -------------------------------------------------------------- decoders
@@ -275,9 +302,9 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
         if (ch + 1 < ch1) load_zeros(ch + 1);
         Ring st1 = st;
         st1.next(S);
-        ok = (!a.w_tma || mbar_wait(smem_u32(&wfull[wr.i]), wr.phase, abort_flag, nullptr)) &&
-             mbar_wait(smem_u32(&empty[st.i]), st.phase ^ 1u, abort_flag, nullptr) &&
-             mbar_wait(smem_u32(&empty[st1.i]), st1.phase ^ 1u, abort_flag, nullptr);
+        ok = (!a.w_tma || mbar_wait(bars.wfull + 8 * wr.i, wr.phase, abort_flag, nullptr)) &&
+             mbar_wait(bars.empty + 8 * st.i, st.phase ^ 1u, abort_flag, nullptr) &&
+             mbar_wait(bars.empty + 8 * st1.i, st1.phase ^ 1u, abort_flag, nullptr);
         if (!ok) break;
         const uint8_t* buf = wring + wr.i * wbytes;
         uint8_t* t0 = smem + st.i * Cfg::STAGE + Cfg::X_BYTES;
@@ -296,9 +323,9 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(smem_u32(&full_a[st.i]));
-          mbar_arrive(smem_u32(&full_a[st1.i]));
-          if (a.w_tma) mbar_arrive(smem_u32(&wempty[wr.i]));
+          mbar_arrive(bars.full_a + 8 * st.i);
+          mbar_arrive(bars.full_a + 8 * st1.i);
+          if (a.w_tma) mbar_arrive(bars.wempty + 8 * wr.i);
         }
         st = st1;
         st.next(S);
@@ -327,7 +354,7 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
         const float here = s;
         if (g + 1 < g1) s = col < p.n ? __ldg(scale + g + 1) : 0.f;
         if (ok) {
-          ok = mbar_wait(smem_u32(&rfull[slot.i]), slot.phase, abort_flag, nullptr);
+          ok = mbar_wait(bars.rfull + 8 * slot.i, slot.phase, abort_flag, nullptr);
           ok = __all_sync(~0u, ok);
         }
         if (!ok) break;
@@ -341,7 +368,7 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&rempty[slot.i]));
+        if (lane == 0) mbar_arrive(bars.rempty + 8 * slot.i);
         slot.next(2);
       }
       if (!ok)
