@@ -19,6 +19,26 @@ struct Ring {
   }
 };
 
+// A float that is needed later (0 where `there` is false): the load is issued
+// here and now, not where the compiler would rather have it.
+__device__ __forceinline__ float load_ahead(const float* p, bool there) {
+  float v;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %2, 0;\n\t"
+      "mov.b32 %0, 0;\n\t"
+      "@p ld.global.nc.f32 %0, [%1];\n\t}"
+      : "=f"(v)
+      : "l"(p), "r"((int)there));
+  return v;
+}
+
+__device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c,
+                                             uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d)
+               : "memory");
+}
+
 // True for one lane of the (converged) warp.  A role that issues tcgen05
 // instructions runs on its whole warp and elects a lane for the issue alone:
 // descriptors and loop state then stay in uniform registers.
@@ -41,6 +61,27 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
           dst),
       "l"(src), "r"(bytes), "r"(bar)
       : "memory");
+}
+
+// Asynchronous copy from this CTA's shared memory to the same cluster's
+// (16-byte aligned, size a multiple of 16), completing on a barrier there.
+__device__ __forceinline__ void bulk_copy_to_peer(uint32_t dst_cluster, uint32_t src, uint32_t bytes,
+                                                  uint32_t bar_cluster) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          dst_cluster),
+      "r"(src), "r"(bytes), "r"(bar_cluster)
+      : "memory");
+}
+
+// Two fp32 multiply-adds: d += (s, s) * v.
+__device__ __forceinline__ void fma_x2(float2& d, float s, float v0, float v1) {
+  uint64_t dd, ss, vv;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(dd) : "f"(d.x), "f"(d.y));
+  asm("mov.b64 %0, {%1, %1};" : "=l"(ss) : "f"(s));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(vv) : "f"(v0), "f"(v1));
+  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(dd) : "l"(ss), "l"(vv));
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(d.x), "=f"(d.y) : "l"(dd));
 }
 
 // A float in the shared memory of a CTA of the cluster.

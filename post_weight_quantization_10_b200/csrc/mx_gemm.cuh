@@ -89,8 +89,8 @@ __global__ void __launch_bounds__(kMxTileThreads)
     k_mx_tile(const __grid_constant__ MxArgs p) {
   constexpr int NSF = kMxBK / MxFormat<FMT>::TILE_K;  // scale tiles per stage and 128 rows
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                             ~static_cast<uintptr_t>(1023));
+  // (an offset, not a cast: the compiler has to see shared memory behind it)
+  uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   const int xt = (p.tn + 127) >> 7;  // 128-row scale tiles of the activations
   const int x_bytes = p.tn * 128;
   const int x_off = 128 * 128, sw_off = x_off + ((x_bytes + 1023) & ~1023),

@@ -78,13 +78,13 @@ bool make_x_map(CUtensorMap* m, const PackedArgs& p, bool bf16, int box_rows) {
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Packed rows as bytes, boxes of a 128-code chunk (16 b bytes) x 128 rows.
-bool make_w_map(CUtensorMap* m, const PackedArgs& p) {
+// Packed rows as bytes, boxes of a 128-code chunk (16 b bytes).
+bool make_w_map(CUtensorMap* m, const PackedArgs& p, int box_rows) {
   auto fn = encode_fn();
   if (!fn) return false;
   cuuint64_t dims[2] = {(cuuint64_t)p.words * 4, (cuuint64_t)p.n};
   cuuint64_t strides[1] = {(cuuint64_t)p.words * 4};
-  cuuint32_t box[2] = {(cuuint32_t)(16 * p.bits), 128};
+  cuuint32_t box[2] = {(cuuint32_t)(16 * p.bits), (cuuint32_t)box_rows};
   cuuint32_t estr[2] = {1, 1};
   const CUtensorMapSwizzle sw = p.bits == 2   ? CU_TENSOR_MAP_SWIZZLE_32B
                                 : p.bits == 4 ? CU_TENSOR_MAP_SWIZZLE_64B
@@ -95,34 +95,36 @@ bool make_w_map(CUtensorMap* m, const PackedArgs& p) {
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <typename X, int TN>
-int launch_gemm_tn(const PackedArgs& p, cudaStream_t st) {
-  using Cfg = PackedCfg<TN>;
+template <typename X, int TN, int C>
+int launch_gemm(const PackedArgs& p, cudaStream_t st) {
+  using Cfg = PackedCfg<TN, C>;
   PackedGemmArgs a;
   a.p = p;
-  a.tiles_m = cdiv(p.m, TN);
+  a.tiles_m = cdiv(p.m, TN * C);
   const long long tiles = (long long)a.tiles_m * cdiv(p.n, 128);
   if (tiles > (1 << 28)) return ADMMQ_ERR_UNSUPPORTED;
   a.tiles = (int)tiles;
   a.chunks = cdiv(p.k, 128);
   a.passes = 128 / p.group;
   a.w_tma = p.words % 4 == 0;
-  int ranks = 1;
-  while (ranks < 8 && a.chunks >= 4 * ranks && tiles * 2 * ranks <= num_sms()) ranks *= 2;
-  a.range = cdiv(a.chunks, ranks);
-  const int room = 226 * 1024, wbytes = 2048 * p.bits;
+  int ranks = C;
+  if (C == 1)
+    while (ranks < 8 && a.chunks >= 4 * ranks && tiles * 2 * ranks <= num_sms()) ranks *= 2;
+  a.range = C == 1 ? cdiv(a.chunks, ranks) : a.chunks;
+  const int room = 226 * 1024, wbytes = 16 * Cfg::ROWS * p.bits;
   a.stages = 4;
   a.wbufs = (room - 1024 - a.stages * Cfg::STAGE - 512) / wbytes;
   if (a.wbufs > 4) a.wbufs = 4;
   if (!make_x_map(&a.x, p, __is_same(X, __nv_bfloat16), TN)) return ADMMQ_ERR_CUDA;
-  if (a.w_tma && !make_w_map(&a.w, p)) return ADMMQ_ERR_CUDA;
+  if (a.w_tma && !make_w_map(&a.w, p, Cfg::ROWS)) return ADMMQ_ERR_CUDA;
   int smem = a.stages * Cfg::STAGE + a.wbufs * wbytes + 1024 + 512;
   smem = tmem_fair_smem(smem, Cfg::TMEM_COLS);
-  auto kern = k_packed_gemm<X, TN>;
+  auto kern = k_packed_gemm<X, TN, C>;
   CK(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
-  const long long grid = ranks > 1 ? tiles * ranks : (tiles < num_sms() ? tiles : num_sms());
+  const int most = C == 1 && ranks > 1 ? a.tiles : num_sms() / ranks;
+  const int clusters = a.tiles < most ? a.tiles : most;
   cudaLaunchConfig_t lc = {};
-  lc.gridDim = dim3((unsigned)grid);
+  lc.gridDim = dim3((unsigned)(clusters * ranks));
   lc.blockDim = dim3(kPackedThreads);
   lc.dynamicSmemBytes = smem;
   lc.stream = st;
@@ -141,9 +143,10 @@ int launch_gemm_tn(const PackedArgs& p, cudaStream_t st) {
 template <typename X>
 int launch_packed(const PackedArgs& p, cudaStream_t st) {
   if (p.m <= kFewTokens) return launch_few<X>(p, st);
-  if (p.m <= 64) return launch_gemm_tn<X, 64>(p, st);
-  if (p.m <= 128) return launch_gemm_tn<X, 128>(p, st);
-  return launch_gemm_tn<X, 256>(p, st);
+  if (p.m <= 64) return launch_gemm<X, 64, 1>(p, st);
+  if (p.m <= 128) return launch_gemm<X, 128, 1>(p, st);
+  if (p.m <= 256) return launch_gemm<X, 256, 1>(p, st);
+  return launch_gemm<X, 256, 2>(p, st);
 }
 
 }  // namespace

@@ -109,4 +109,75 @@ __device__ __forceinline__ void decode32(const uint32_t (&w)[B], float zero, uin
   }
 }
 
+// As decode32, but in column order: out[j] holds codes 2 j and 2 j + 1.  Two
+// windows of the bit stream, one code apart, side by side: a mask then takes
+// neighbouring codes from the two halves.  (For 2 and 4 bits a byte of the
+// word and of the word shifted by one code serve as the windows.)
+template <typename X, int B>
+__device__ __forceinline__ void decode32_in_order(const uint32_t (&w)[B], float zero,
+                                                  uint32_t (&out)[16]) {
+  constexpr bool BF = __is_same(X, __nv_bfloat16);
+  if constexpr (BF && B == 8) {
+    const float zz = 8388608.f + zero;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      const uint32_t sel = 0x7650u + 2 * (j & 1);
+      const float lo = __uint_as_float(__byte_perm(w[j >> 1], 0x4B000000u, sel)) - zz;
+      const float hi = __uint_as_float(__byte_perm(w[j >> 1], 0x4B000000u, sel + 1)) - zz;
+      const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+      out[j] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+  } else {
+    constexpr uint32_t MASK = (1u << B) - 1u;
+    constexpr int MANTISSA = BF ? 7 : 10;
+    constexpr bool BYTES = B == 2 || B == 4 || B == 8;
+    constexpr int PER = BYTES ? 8 / B : 16 / B;        // codes of a window
+    constexpr int PAIRS = (PER + 1) / 2;               // pairs (even code, next one) of two windows
+    constexpr int FIT = (MANTISSA - B) / (2 * B) + 1;  // of them, without a shift
+    constexpr uint32_t MAGIC = BF ? 0x43004300u : 0x64006400u;
+    constexpr float BASE = BF ? 128.f : 1024.f;
+    X minus[FIT];
+#pragma unroll
+    for (int f = 0; f < FIT; ++f) {
+      const float c = -(BASE / (float)(1 << (2 * f * B)) + zero);
+      if constexpr (BF)
+        minus[f] = __float2bfloat16_rn(c);
+      else
+        minus[f] = __float2half_rn(c);
+    }
+#pragma unroll
+    for (int j0 = 0; j0 < 16; j0 += PAIRS) {
+      uint32_t t;
+      if constexpr (B == 8) {
+        t = __byte_perm(w[j0 >> 1], 0u, j0 & 1 ? 0x4342 : 0x4140);
+      } else if constexpr (BYTES) {
+        const uint32_t v = w[2 * j0 * B / 32];
+        const int byte = 2 * j0 * B / 8 % 4;
+        t = __byte_perm(v, v >> B, byte | (byte << 4) | ((byte + 4) << 8) | ((byte + 4) << 12));
+      } else {
+        t = __byte_perm(bits_at<B>(w, 2 * j0 * B), bits_at<B>(w, (2 * j0 + 1) * B), 0x5410);
+      }
+#pragma unroll
+      for (int i = 0; i < PAIRS; ++i) {
+        if (j0 + i >= 16) break;
+        const int f = i % FIT;
+        const uint32_t m = (MASK | (MASK << 16)) << (2 * f * B);
+        const uint32_t v = and_or(t >> (2 * (i - f) * B), m, MAGIC);
+        if constexpr (BF) {
+          const X up = __float2bfloat16_rn(1.f / (float)(1 << (2 * f * B)));
+          const __nv_bfloat162 d = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&v),
+                                           __halves2bfloat162(up, up),
+                                           __halves2bfloat162(minus[f], minus[f]));
+          out[j0 + i] = *reinterpret_cast<const uint32_t*>(&d);
+        } else {
+          const X up = __float2half_rn(1.f / (float)(1 << (2 * f * B)));
+          const __half2 d = __hfma2(*reinterpret_cast<const __half2*>(&v), __halves2half2(up, up),
+                                    __halves2half2(minus[f], minus[f]));
+          out[j0 + i] = *reinterpret_cast<const uint32_t*>(&d);
+        }
+      }
+    }
+  }
+}
+
 }  // namespace admmq

@@ -33,14 +33,20 @@ constexpr int kPackedThreads = 512;
 //   0  warp 0: TMA producer, warp 1: MMA issuer
 //   1  decoders
 //   2, 3  consumers: thread = accumulator row, half of the tile's tokens each
-// One output tile of 128 x TN per cluster and turn; a cluster's CTAs share the
-// reduction (contiguous ranges of chunks) and add their tiles in rank order
-// through distributed shared memory.  A cluster of one goes on to further tiles.
-template <int TN>
+// Turning codes into operands takes about as many instructions as there are
+// cycles in the MMAs that use them, so with C = 2 a cluster of two CTAs works
+// on the same 128 weight rows and two token tiles: each decodes half of the
+// rows and copies them into the other's shared memory.  Clusters go from tile
+// to tile.  With C = 1 (one token tile) the CTAs of a cluster share the
+// reduction instead (contiguous ranges of chunks) and add their tiles in rank
+// order through distributed shared memory.
+template <int TN, int C>
 struct PackedCfg {
   static constexpr int HALF = TN / 2;
   static constexpr int X_BYTES = TN * 128, A_BYTES = 128 * 128, STAGE = X_BYTES + A_BYTES;
   static constexpr int TMEM_COLS = 2 * TN;
+  static constexpr int ROWS = 128 / C;         // weight rows that a CTA decodes
+  static constexpr int STEPS = ROWS / 32;      // of 8 rows, per decoder warp
 };
 
 // Words of unit q (32 codes) of a row of a packed chunk in shared memory.  TMA
@@ -74,40 +80,24 @@ __device__ __forceinline__ void chunk_words(const uint8_t* buf, int row, int q, 
   }
 }
 
-// One chunk (128 rows x 128 columns) by the four decoder warps into the
-// operand tiles of its two stages.
+// A chunk's words of two of this lane's rows (unit q of rows row and row + 8)
+// to 16-bit pairs in column order.
 template <typename X, int B>
-__device__ __forceinline__ void decode_chunk(const PackedGemmArgs& a, const uint8_t* buf,
-                                             uint8_t* tile0, uint8_t* tile1, long long row0,
-                                             int chunk, const float (&zero)[4]) {
-  const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3;
-  const int q = lane >> 3;
-  uint8_t* tile = q < 2 ? tile0 : tile1;
+__device__ __forceinline__ void decode_chunk(const PackedGemmArgs& a, const uint8_t* buf, int row,
+                                             int q, long long row0, int chunk, const float* zero,
+                                             uint32_t (&v)[2][16]) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int row = warp * 32 + i * 8 + (lane & 7);
-    uint32_t w[B], v[16];
+  for (int i = 0; i < 2; ++i) {
+    uint32_t w[B];
     if (a.w_tma) {
-      chunk_words<B>(buf, row, q, w);
+      chunk_words<B>(buf, row + 8 * i, q, w);
     } else {
-      const bool in = row0 + row < a.p.n && chunk * 128 + 32 * q < a.p.k;
-      const uint32_t* src = a.p.packed + (row0 + row) * a.p.words + (chunk * 4 + q) * B;
+      const bool in = row0 + row + 8 * i < a.p.n && chunk * 128 + 32 * q < a.p.k;
+      const uint32_t* src = a.p.packed + (row0 + row + 8 * i) * a.p.words + (chunk * 4 + q) * B;
 #pragma unroll
       for (int j = 0; j < B; ++j) w[j] = in ? __ldg(src + j) : 0u;
     }
-    decode32<X, B>(w, zero[i], v);
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      // columns 8 c .. 8 c + 7 of the unit, in order again
-      const int h = 4 * (c & 1);
-      const uint32_t sel = c < 2 ? 0x5410 : 0x7632;
-      uint4 o;
-      o.x = __byte_perm(v[2 * h], v[2 * h + 1], sel);
-      o.y = __byte_perm(v[2 * h + 2], v[2 * h + 3], sel);
-      o.z = __byte_perm(v[2 * h + 4], v[2 * h + 5], sel);
-      o.w = __byte_perm(v[2 * h + 6], v[2 * h + 7], sel);
-      *reinterpret_cast<uint4*>(tile + row * 128 + ((((q & 1) * 4 + c) ^ (row & 7)) << 4)) = o;
-    }
+    decode32_in_order<X, B>(w, zero[i], v[i]);
   }
 }
 
@@ -131,11 +121,11 @@ struct PackedBars {
 };
 
 // The MMA warp's loop: 8 MMAs of K = 16 per chunk, PASSES groups.
-template <typename X, int TN, int PASSES>
+template <typename X, int TN, int C, int PASSES>
 __device__ __forceinline__ bool issue_mmas(const PackedGemmArgs& a, int ch0, int ch1, int tile0,
                                            int tile_step, uint32_t tmem, const uint8_t* smem,
                                            const PackedBars& bars, volatile int* abort_flag) {
-  using Cfg = PackedCfg<TN>;
+  using Cfg = PackedCfg<TN, C>;
   constexpr uint32_t IDESC = idesc_f32acc(__is_same(X, __nv_bfloat16) ? 1 : 0, 128, TN, false, false);
   constexpr int PER = 8 / PASSES;  // MMAs of a group
   const uint64_t dx0 = smem_desc_sw128(smem_u32(smem), 16, 1024);
@@ -172,7 +162,11 @@ __device__ __forceinline__ bool issue_mmas(const PackedGemmArgs& a, int ch0, int
           }
         }
         if (!__all_sync(~0u, ok)) return false;
-        if (elect_one()) mma_commit(bars.empty + 8 * st.i);
+        if (elect_one()) {  // a stage's decoders write to every CTA that uses it
+          if (C == 1) mma_commit(bars.empty + 8 * st.i);
+#pragma unroll
+          for (int c = 0; c < (C > 1 ? C : 0); ++c) mma_commit(cluster_addr(bars.empty + 8 * st.i, c));
+        }
         __syncwarp();
         st.next(a.stages);
       }
@@ -181,15 +175,32 @@ __device__ __forceinline__ bool issue_mmas(const PackedGemmArgs& a, int ch0, int
   return true;
 }
 
-template <typename X, int TN>
+__device__ __forceinline__ void put(float* p, float v) { *p = v; }
+__device__ __forceinline__ void put(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+__device__ __forceinline__ void put(__half* p, float v) { *p = __float2half_rn(v); }
+
+// Column `col` of the output, tokens token0 .. + HALF - 1.
+template <int HALF, typename T>
+__device__ __forceinline__ void store_column(T* out, const PackedArgs& p, int token0, long long col,
+                                             const float2 (&acc)[HALF / 2]) {
+  T* at = out + (long long)token0 * p.n + col;
+  const int tokens = p.m - token0;
+#pragma unroll
+  for (int i = 0; i < HALF; ++i) {
+    if (i < tokens) put(at, i & 1 ? acc[i / 2].y : acc[i / 2].x);
+    at += p.n;
+  }
+}
+
+template <typename X, int TN, int C>
 __global__ void __launch_bounds__(kPackedThreads, 1)
     k_packed_gemm(const __grid_constant__ PackedGemmArgs a) {
-  using Cfg = PackedCfg<TN>;
+  using Cfg = PackedCfg<TN, C>;
   const PackedArgs& p = a.p;
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                             ~static_cast<uintptr_t>(1023));
-  const int S = a.stages, NW = a.wbufs, wbytes = 2048 * p.bits;
+  // (an offset, not a cast: the compiler has to see shared memory behind it)
+  uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  const int S = a.stages, NW = a.wbufs, wbytes = 16 * Cfg::ROWS * p.bits;
   uint8_t* wring = smem + S * Cfg::STAGE;
   const PackedBars bars(smem_u32(wring + NW * wbytes), S, NW);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(wring + NW * wbytes + (bars.end - bars.full_x));
@@ -199,14 +210,16 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
   uint32_t rank, ranks;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
   asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(ranks));
+  // with C > 1 `tiles` counts clusters of tiles: C token tiles of 128 columns
   const int tile0 = blockIdx.x / ranks, tile_step = gridDim.x / ranks;
-  const int ch0 = rank * a.range, ch1 = min(ch0 + a.range, a.chunks);
+  const int ch0 = C > 1 ? 0 : rank * a.range, ch1 = min(ch0 + a.range, a.chunks);
+  const int part0 = C > 1 ? rank * Cfg::ROWS : 0;  // first of the weight rows decoded here
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
       mbar_init(bars.full_x + 8 * s, 1);
       mbar_init(bars.full_a + 8 * s, 4);
-      mbar_init(bars.empty + 8 * s, 1);
+      mbar_init(bars.empty + 8 * s, C);
     }
     for (int i = 0; i < NW; ++i) {
       mbar_init(bars.wfull + 8 * i, 1);
@@ -222,6 +235,7 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
   }
   if (warp == 1) tmem_alloc(smem_u32(tmem_slot), Cfg::TMEM_COLS);
   __syncthreads();
+  if (C > 1) cluster_sync();  // the peers' barriers exist
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const int wg = warp >> 2;
@@ -234,7 +248,7 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
       Ring x, w;  // a fresh ring's buffers count as emptied once: parity 1
       int loads = 0, chunks = 0;
       for (int tile = tile0; tile < a.tiles && ok; tile += tile_step) {
-        const int tn = tile / a.tiles_m, tm = tile - tn * a.tiles_m;
+        const int tn = tile / a.tiles_m, tm = (tile - tn * a.tiles_m) * C + (C > 1 ? rank : 0);
         for (int ch = ch0; ch < ch1 && ok; ++ch) {
           if (a.w_tma) {
             const uint32_t bar = bars.wfull + 8 * w.i;
@@ -243,7 +257,7 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
               break;
             }
             mbar_arrive_expect_tx(bar, wbytes);
-            tma_load_2d(smem_u32(wring + w.i * wbytes), &a.w, ch * 16 * p.bits, tn * 128, bar);
+            tma_load_2d(smem_u32(wring + w.i * wbytes), &a.w, ch * 16 * p.bits, tn * 128 + part0, bar);
             w.next(NW);
             ++chunks;
           }
@@ -269,9 +283,9 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
       }
     } else if (warp == 1) {
       // -------------------------------------------------------- MMA issuer
-      const bool ok = a.passes == 1   ? issue_mmas<X, TN, 1>(a, ch0, ch1, tile0, tile_step, tmem, smem, bars, abort_flag)
-                      : a.passes == 2 ? issue_mmas<X, TN, 2>(a, ch0, ch1, tile0, tile_step, tmem, smem, bars, abort_flag)
-                                      : issue_mmas<X, TN, 4>(a, ch0, ch1, tile0, tile_step, tmem, smem, bars, abort_flag);
+      const bool ok = a.passes == 1   ? issue_mmas<X, TN, C, 1>(a, ch0, ch1, tile0, tile_step, tmem, smem, bars, abort_flag)
+                      : a.passes == 2 ? issue_mmas<X, TN, C, 2>(a, ch0, ch1, tile0, tile_step, tmem, smem, bars, abort_flag)
+                                      : issue_mmas<X, TN, C, 4>(a, ch0, ch1, tile0, tile_step, tmem, smem, bars, abort_flag);
       (void)ok;
       if (elect_one()) mma_commit(bars.drain);
       __syncwarp();
@@ -280,56 +294,96 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
   } else if (wg == 1) {
     // -------------------------------------------------------------- decoders
     if constexpr (TN == 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-    bool ok = true;
+    // The codes are decoded into registers while the MMAs still read the stage
+    // that they will go to; what is left once it is free are the stores.
     Ring st, wr;
+    bool ok = true;
     const int q = lane >> 3;
+    const int row = (warp - 4) * Cfg::STEPS * 8 + (lane & 7);  // of the part decoded here
     const int group_shift = __ffs(p.group) - 1;
+    uint32_t to[4];  // of this lane's four 16-byte pieces in a stage's operand tile
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      to[c] = smem_u32(smem) + Cfg::X_BYTES + (part0 + row) * 128 +
+              ((((q & 1) * 4 + c) ^ (row & 7)) << 4);
     for (int tile = tile0; tile < a.tiles && ok; tile += tile_step) {
-      const long long row0 = (long long)(tile / a.tiles_m) * 128;
-      float next[4], zero[4];
+      const long long row0 = (long long)(tile / a.tiles_m) * 128 + part0;
+      const float* zeros = p.zero + (row0 + row) * p.groups;
+      float next[Cfg::STEPS], zero[Cfg::STEPS];
       auto load_zeros = [&](int ch) {
         const int k = ch * 128 + 32 * q;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const long long row = row0 + (warp & 3) * 32 + i * 8 + (lane & 7);
-          next[i] = row < p.n && k < p.k ? __ldg(p.zero + row * p.groups + (k >> group_shift)) : 0.f;
-        }
+        for (int i = 0; i < Cfg::STEPS; ++i)
+          next[i] = load_ahead(zeros + 8 * i * p.groups + (k >> group_shift),
+                               row0 + row + 8 * i < p.n && k < p.k);
       };
       load_zeros(ch0);
       for (int ch = ch0; ch < ch1; ++ch) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) zero[i] = next[i];
+        for (int i = 0; i < Cfg::STEPS; ++i) zero[i] = next[i];
         if (ch + 1 < ch1) load_zeros(ch + 1);
+        if (a.w_tma && !mbar_wait(bars.wfull + 8 * wr.i, wr.phase, abort_flag, nullptr)) {
+          ok = false;
+          break;
+        }
+        const uint8_t* buf = wring + wr.i * wbytes;
         Ring st1 = st;
         st1.next(S);
-        ok = (!a.w_tma || mbar_wait(bars.wfull + 8 * wr.i, wr.phase, abort_flag, nullptr)) &&
-             mbar_wait(bars.empty + 8 * st.i, st.phase ^ 1u, abort_flag, nullptr) &&
-             mbar_wait(bars.empty + 8 * st1.i, st1.phase ^ 1u, abort_flag, nullptr);
-        if (!ok) break;
-        const uint8_t* buf = wring + wr.i * wbytes;
-        uint8_t* t0 = smem + st.i * Cfg::STAGE + Cfg::X_BYTES;
-        uint8_t* t1 = smem + st1.i * Cfg::STAGE + Cfg::X_BYTES;
-        switch (p.bits) {
-          case 1: decode_chunk<X, 1>(a, buf, t0, t1, row0, ch, zero); break;
-          case 2: decode_chunk<X, 2>(a, buf, t0, t1, row0, ch, zero); break;
-          case 3: decode_chunk<X, 3>(a, buf, t0, t1, row0, ch, zero); break;
-          case 4: decode_chunk<X, 4>(a, buf, t0, t1, row0, ch, zero); break;
-          case 5: decode_chunk<X, 5>(a, buf, t0, t1, row0, ch, zero); break;
-          case 6: decode_chunk<X, 6>(a, buf, t0, t1, row0, ch, zero); break;
-          case 7: decode_chunk<X, 7>(a, buf, t0, t1, row0, ch, zero); break;
-          default: decode_chunk<X, 8>(a, buf, t0, t1, row0, ch, zero); break;
+        const Ring mine = q < 2 ? st : st1;  // units 0, 1 go to the first stage, 2, 3 to the second
+        const uint32_t stage = mine.i * Cfg::STAGE;
+#pragma unroll
+        for (int i = 0; i < Cfg::STEPS; i += 2) {
+          uint32_t v[2][16];
+          const float* z = zero + i;
+          switch (p.bits) {
+            case 1: decode_chunk<X, 1>(a, buf, row + 8 * i, q, row0, ch, z, v); break;
+            case 2: decode_chunk<X, 2>(a, buf, row + 8 * i, q, row0, ch, z, v); break;
+            case 3: decode_chunk<X, 3>(a, buf, row + 8 * i, q, row0, ch, z, v); break;
+            case 4: decode_chunk<X, 4>(a, buf, row + 8 * i, q, row0, ch, z, v); break;
+            case 5: decode_chunk<X, 5>(a, buf, row + 8 * i, q, row0, ch, z, v); break;
+            case 6: decode_chunk<X, 6>(a, buf, row + 8 * i, q, row0, ch, z, v); break;
+            case 7: decode_chunk<X, 7>(a, buf, row + 8 * i, q, row0, ch, z, v); break;
+            default: decode_chunk<X, 8>(a, buf, row + 8 * i, q, row0, ch, z, v); break;
+          }
+          if (i == 0)
+            ok = C > 1 ? mbar_wait_cluster(bars.empty + 8 * mine.i, mine.phase ^ 1u, abort_flag, nullptr)
+                       : mbar_wait(bars.empty + 8 * mine.i, mine.phase ^ 1u, abort_flag, nullptr);
+          if (!ok) break;
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              st_shared_v4(to[c] + stage + (i + j) * 8 * 128, v[j][4 * c], v[j][4 * c + 1],
+                           v[j][4 * c + 2], v[j][4 * c + 3]);
         }
-        // the MMA reads what these stores wrote through the async proxy
+        if (!__all_sync(~0u, ok)) {
+          ok = false;
+          break;
+        }
+        // the MMA and the copies read what these stores wrote through the async proxy
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(bars.full_a + 8 * st.i);
-          mbar_arrive(bars.full_a + 8 * st1.i);
           if (a.w_tma) mbar_arrive(bars.wempty + 8 * wr.i);
+          if (C == 1) {
+            mbar_arrive(bars.full_a + 8 * st.i);
+            mbar_arrive(bars.full_a + 8 * st1.i);
+          } else {
+            // this warp's rows to the other CTA, the other CTA's expected here
+            constexpr uint32_t BYTES = Cfg::STEPS * 8 * 128;
+            const uint32_t src = smem_u32(smem) + Cfg::X_BYTES + (part0 + (warp - 4) * Cfg::STEPS * 8) * 128;
+            const uint32_t peer = rank ^ 1;
+            mbar_arrive_expect_tx(bars.full_a + 8 * st.i, BYTES);
+            mbar_arrive_expect_tx(bars.full_a + 8 * st1.i, BYTES);
+            bulk_copy_to_peer(cluster_addr(src + st.i * Cfg::STAGE, peer), src + st.i * Cfg::STAGE,
+                              BYTES, cluster_addr(bars.full_a + 8 * st.i, peer));
+            bulk_copy_to_peer(cluster_addr(src + st1.i * Cfg::STAGE, peer), src + st1.i * Cfg::STAGE,
+                              BYTES, cluster_addr(bars.full_a + 8 * st1.i, peer));
+          }
         }
+        wr.next(NW);
         st = st1;
         st.next(S);
-        wr.next(NW);
       }
     }
   } else {
@@ -342,17 +396,17 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
     bool ok = true;
     Ring slot;
     for (int tile = tile0; tile < a.tiles; tile += tile_step) {
-      const int tn = tile / a.tiles_m, tm = tile - tn * a.tiles_m;
+      const int tn = tile / a.tiles_m, tm = (tile - tn * a.tiles_m) * C + (C > 1 ? rank : 0);
       const long long col = (long long)tn * 128 + row;
-      float acc[HALF];
+      float2 acc[HALF / 2];
 #pragma unroll
-      for (int i = 0; i < HALF; ++i) acc[i] = 0.f;
+      for (int i = 0; i < HALF / 2; ++i) acc[i] = make_float2(0.f, 0.f);
       const int g0 = ch0 * a.passes, g1 = min(ch1 * a.passes, p.groups);
       const float* scale = p.scale + col * p.groups;
-      float s = col < p.n && g0 < g1 ? __ldg(scale + g0) : 0.f;
+      float s = load_ahead(scale + g0, col < p.n && g0 < g1);
       for (int g = g0; g < g1; ++g) {
         const float here = s;
-        if (g + 1 < g1) s = col < p.n ? __ldg(scale + g + 1) : 0.f;
+        s = load_ahead(scale + g + 1, col < p.n && g + 1 < g1);
         if (ok) {
           ok = mbar_wait(bars.rfull + 8 * slot.i, slot.phase, abort_flag, nullptr);
           ok = __all_sync(~0u, ok);
@@ -364,7 +418,7 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
           float v[16];
           tmem_ld16(ta + slot.i * TN + 16 * j, v);
 #pragma unroll
-          for (int i = 0; i < 16; ++i) acc[16 * j + i] += here * v[i];
+          for (int i = 0; i < 8; ++i) fma_x2(acc[8 * j + i], here, v[2 * i], v[2 * i + 1]);
         }
         tc_fence_before();
         __syncwarp();
@@ -373,23 +427,30 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
       }
       if (!ok)
 #pragma unroll
-        for (int i = 0; i < HALF; ++i) acc[i] = __int_as_float(0x7FFFFFFF);
-      if (ranks == 1) {
+        for (int i = 0; i < HALF / 2; ++i)
+          acc[i] = make_float2(__int_as_float(0x7FFFFFFF), __int_as_float(0x7FFFFFFF));
+      if (C > 1 || ranks == 1) {
         const int token0 = tm * TN + half * HALF;
         if (col < p.n) {
-#pragma unroll
-          for (int i = 0; i < HALF; ++i)
-            if (token0 + i < p.m) put_out(p, (long long)(token0 + i) * p.n + col, acc[i]);
+          if (p.out_dtype == ADMMQ_DTYPE_F32)
+            store_column<HALF>((float*)p.out, p, token0, col, acc);
+          else if (p.out_dtype == ADMMQ_DTYPE_BF16)
+            store_column<HALF>((__nv_bfloat16*)p.out, p, token0, col, acc);
+          else
+            store_column<HALF>((__half*)p.out, p, token0, col, acc);
         }
       } else {
         float* part = reinterpret_cast<float*>(smem);  // [TN][128], over the used stages
 #pragma unroll
-        for (int i = 0; i < HALF; ++i) part[(half * HALF + i) * 128 + row] = acc[i];
+        for (int i = 0; i < HALF; ++i)
+          part[(half * HALF + i) * 128 + row] = i & 1 ? acc[i / 2].y : acc[i / 2].x;
       }
     }
   }
-  if (ranks > 1) {
-    __syncwarp();
+  __syncwarp();
+  if (C > 1) {
+    cluster_sync();  // no copy or arrival from here is under way to the other CTA
+  } else if (ranks > 1) {
     cluster_sync();
     const int row = threadIdx.x & 127;
     const long long col = (long long)(tile0 / a.tiles_m) * 128 + row;
