@@ -189,6 +189,51 @@ bool make_codes_map(CUtensorMap* m, const void* ptr, int k, int64_t rows, int bo
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Scale tiles as rows of 128 words, boxes of `tiles` rows; rows out of range
+// read as zero.
+bool make_scales_map(CUtensorMap* m, const void* ptr, int64_t tiles, int box_rows) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[2] = {kScaleTile / 4, (cuuint64_t)tiles};
+  cuuint64_t strides[1] = {kScaleTile};
+  cuuint32_t box[2] = {kScaleTile / 4, (cuuint32_t)box_rows};
+  cuuint32_t estr[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<void*>(ptr), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int FMT, typename T>
+int launch_pair(const uint8_t* w_codes, const uint8_t* x_codes, const MxArgs& q, cudaStream_t st) {
+  using Cfg = MxPairCfg<FMT>;
+  MxPairArgs p;
+  p.gw = q.gw;
+  p.gx = q.gx;
+  p.out = q.out;
+  p.m = q.m;
+  p.n = q.n;
+  p.k = q.k;
+  p.tiles_m = cdiv(q.m, 256);
+  const long long tiles = (long long)p.tiles_m * cdiv(q.n, 256);
+  if (tiles > (1 << 28)) return ADMMQ_ERR_UNSUPPORTED;
+  p.tiles = (int)tiles;
+  p.kblocks = q.kblocks;
+  p.col_tiles = q.col_tiles;
+  p.stages = (226 * 1024 - 1024) / (Cfg::STAGE + 16);
+  if (!make_codes_map(&p.w, w_codes, q.k, q.n, 128) || !make_codes_map(&p.x, x_codes, q.k, q.m, 128) ||
+      !make_scales_map(&p.ws, q.w_scale, (int64_t)cdiv(q.n, 128) * q.col_tiles, Cfg::NSF) ||
+      !make_scales_map(&p.xs, q.x_scale, (int64_t)cdiv(q.m, 128) * q.col_tiles, Cfg::NSF))
+    return ADMMQ_ERR_CUDA;
+  const int smem = tmem_fair_smem(p.stages * (Cfg::STAGE + 16) + 1024 + 64, 512);
+  auto kern = k_mx_pair<FMT, T>;
+  CK(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+  const int pairs = num_sms() / 2;
+  count_launch();
+  kern<<<2 * (p.tiles < pairs ? p.tiles : pairs), kMxPairThreads, smem, st>>>(p);
+  CK(cudaGetLastError());
+  return ADMMQ_OK;
+}
+
 template <int FMT, typename T>
 int launch_tile(MxArgs& p, cudaStream_t st) {
   constexpr int NSF = kMxBK / MxFormat<FMT>::TILE_K;
@@ -326,9 +371,12 @@ int admmq_mx_matmul(const uint8_t* a_codes, const uint8_t* a_scale, const float*
   p.tiles_n = cdiv(n, 128);
   p.kblocks = cdiv(k, kMxBK);
   p.col_tiles = cdiv(k, mx_tile_k(fmt));
-  if (!make_codes_map(&p.w, b_codes, k, n, 128) || !make_codes_map(&p.x, a_codes, k, m, p.tn))
+  const bool pair = m > 128;
+  if (!pair && (!make_codes_map(&p.w, b_codes, k, n, 128) || !make_codes_map(&p.x, a_codes, k, m, p.tn)))
     return ADMMQ_ERR_CUDA;
-#define PRODUCT(FMT, T) rc = launch_tile<FMT, T>(p, (cudaStream_t)stream)
+#define PRODUCT(FMT, T)                                                            \
+  rc = pair ? launch_pair<FMT, T>(b_codes, a_codes, p, (cudaStream_t)stream)       \
+            : launch_tile<FMT, T>(p, (cudaStream_t)stream)
   MX_DISPATCH(fmt, out_dtype, PRODUCT)
 #undef PRODUCT
   return rc;

@@ -156,37 +156,43 @@ __global__ void __launch_bounds__(kMxTileThreads)
           mbar_wait_drain(smem_u32(&full[j % p.stages]), (uint32_t)(j / p.stages) & 1u);
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      const uint32_t sfw = tmem + ((p.tn + 31) & ~31), sfx = sfw + 4 * NSF;
-      Ring r;
-      for (int kb = kb0; kb < kb1; ++kb) {
-        if (!mbar_wait(smem_u32(&full[r.i]), r.phase, abort_flag, nullptr)) break;
-        tc_fence_after();
-        const uint32_t st = smem_u32(smem + r.i * p.stage_bytes);
-        const uint64_t dw = smem_desc_sw128(st, 16, 1024), dx = smem_desc_sw128(st + x_off, 16, 1024);
-        const uint64_t dsw = scale_desc(st + sw_off), dsx = scale_desc(st + sx_off);
-        const int steps = min(4, (p.k - kb * kMxBK + 63) >> 6);
-        const int tiles = min(NSF, p.col_tiles - kb * NSF);
+    const uint32_t sfw = tmem + ((p.tn + 31) & ~31), sfx = sfw + 4 * NSF;
+    const uint64_t dw0 = smem_desc_sw128(smem_u32(smem), 16, 1024);
+    const uint64_t dx0 = smem_desc_sw128(smem_u32(smem) + x_off, 16, 1024);
+    const uint64_t dsw0 = scale_desc(smem_u32(smem) + sw_off), dsx0 = scale_desc(smem_u32(smem) + sx_off);
+    Ring r;
+    for (int kb = kb0; kb < kb1; ++kb) {
+      const bool ok = mbar_wait(smem_u32(&full[r.i]), r.phase, abort_flag, nullptr);
+      if (!__all_sync(~0u, ok)) break;
+      tc_fence_after();
+      const uint32_t at = r.i * (p.stage_bytes >> 4);
+      const int steps = min(4, (p.k - kb * kMxBK + 63) >> 6);
+      const int tiles = min(NSF, p.col_tiles - kb * NSF);
+      if (elect_one()) {
 #pragma unroll
         for (int i = 0; i < NSF; ++i) {
-          if (i >= tiles) break;
-          tmem_copy_scales(sfw + 4 * i, dsw + i * (kScaleTile >> 4));
-          for (int j = 0; j < xt; ++j)
-            tmem_copy_scales(sfx + 4 * (i * xt + j), dsx + (j * NSF + i) * (kScaleTile >> 4));
+          if (i < tiles) {
+            tmem_copy_scales(sfw + 4 * i, dsw0 + at + i * (kScaleTile >> 4));
+            tmem_copy_scales(sfx + 4 * i * xt, dsx0 + at + i * (kScaleTile >> 4));
+            if (xt > 1)
+              tmem_copy_scales(sfx + 4 * (i * xt + 1), dsx0 + at + (NSF + i) * (kScaleTile >> 4));
+          }
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          if (j >= steps) break;
-          const int at = FMT == MX_MXFP4 ? j >> 1 : j;
-          const uint32_t sf = FMT == MX_MXFP4 ? 2u * (j & 1) : 0u;
-          mma_mx<FMT>(tmem, dw + 2 * j, dx + 2 * j, idesc_mx<FMT>(128, p.tn, sf), sfw + 4 * at,
-                      sfx + 4 * at * xt, (kb > kb0 || j > 0) ? 1u : 0u);
+          if (j < steps) {
+            const int t = FMT == MX_MXFP4 ? j >> 1 : j;
+            const uint32_t sf = FMT == MX_MXFP4 ? 2u * (j & 1) : 0u;
+            mma_mx<FMT>(tmem, dw0 + at + 2 * j, dx0 + at + 2 * j, idesc_mx<FMT>(128, p.tn, sf),
+                        sfw + 4 * t, sfx + 4 * t * xt, (kb > kb0 || j > 0) ? 1u : 0u);
+          }
         }
         mma_commit(smem_u32(&empty[r.i]));
-        r.next(p.stages);
       }
-      mma_commit(smem_u32(done));
+      __syncwarp();
+      r.next(p.stages);
     }
+    if (elect_one()) mma_commit(smem_u32(done));
   }
   __syncwarp();
   // ------------------------------------------------------------- epilogue
@@ -233,6 +239,241 @@ __global__ void __launch_bounds__(kMxTileThreads)
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, p.tmem_cols);
+  }
+}
+
+// --------------------------------------------------------------- many tokens
+
+__device__ __forceinline__ void tmem_copy_scales_pair(uint32_t taddr, uint64_t desc) {
+  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc)
+               : "memory");
+}
+template <int FMT>
+__device__ __forceinline__ void mma_mx_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                            uint32_t idesc, uint32_t sfa, uint32_t sfb,
+                                            uint32_t accumulate) {
+  if (FMT == MX_MXFP4)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], "
+        "[%5], p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, "
+        "[%4], [%5], p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+}
+
+struct MxPairArgs {
+  CUtensorMap w, x, ws, xs;    // codes and scale tiles (512-byte rows)
+  const float *gw, *gx;
+  void* out;
+  int m, n, k;
+  int tiles_m, tiles;          // 256-token tiles; all tiles (token tiles of 256 columns in turn)
+  int kblocks, col_tiles, stages;
+};
+
+constexpr int kMxPairThreads = 320;
+
+template <int FMT>
+struct MxPairCfg {
+  static constexpr int NSF = kMxBK / MxFormat<FMT>::TILE_K;  // scale tiles per stage and 128 rows
+  static constexpr int CODES = 128 * 128;                    // bytes of 128 rows of a stage
+  static constexpr int X_OFF = CODES, SW_OFF = 2 * CODES, SX_OFF = SW_OFF + NSF * kScaleTile;
+  static constexpr int BYTES = SX_OFF + 2 * NSF * kScaleTile;  // loaded per CTA and stage
+  static constexpr int STAGE = (BYTES + 1023) & ~1023;
+};
+
+// Pairs of CTAs (2-SM MMAs) go from tile to tile of 256 output columns x 256
+// tokens.  Each CTA stages its 128 weight rows, its 128 of the tokens, the
+// scales of those weight rows and of all the tokens; the leader issues the
+// scale copies and MMAs for both; each CTA's tensor memory holds its 128
+// columns' accumulators for the 256 tokens (256 of its 512 tensor-memory
+// columns; a second accumulator would leave no room for the scales).  The
+// epilogue takes the whole accumulator into registers, frees it for the next
+// tile's MMAs and stores from there.
+//   warp 0  TMA producer    warp 1  MMA issuer    warps 2-9  epilogue
+template <int FMT, typename T>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxPairThreads, 1)
+    k_mx_pair(const __grid_constant__ MxPairArgs p) {
+  using Cfg = MxPairCfg<FMT>;
+  constexpr int NSF = Cfg::NSF;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  const int S = p.stages;
+  const uint32_t base = smem_u32(smem);
+  const uint32_t full = base + S * Cfg::STAGE, empty = full + 8 * S, dfull = empty + 8 * S,
+                 dempty = dfull + 8, drain = dempty + 8;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + S * Cfg::STAGE + 16 * S + 24);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const int pair0 = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(full + 8 * s, 1);
+      mbar_init(empty + 8 * s, 1);
+    }
+    mbar_init(dfull, 1);
+    mbar_init(dempty, 16);
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) tmem_alloc_pair(smem_u32(tmem_slot), 512);
+  __syncthreads();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      bool ok = true;
+      Ring r;
+      int loads = 0;
+      const uint32_t full0 = cluster_addr(full, 0);
+      for (int tile = pair0; tile < p.tiles && ok; tile += pairs) {
+        const int tn = tile / p.tiles_m, tm = tile - tn * p.tiles_m;
+        const int w_row = tn * 256 + (int)rank * 128, x_row = tm * 256 + (int)rank * 128;
+        int ws = (tn * 2 + (int)rank) * p.col_tiles, xs0 = tm * 2 * p.col_tiles;
+        for (int kb = 0; kb < p.kblocks; ++kb, ++loads) {
+          if (!mbar_wait(empty + 8 * r.i, r.phase ^ 1u, abort_flag, nullptr)) {
+            ok = false;
+            break;
+          }
+          const uint32_t st = base + r.i * Cfg::STAGE, bar = full0 + 8 * r.i;
+          if (rank == 0) mbar_arrive_expect_tx(full + 8 * r.i, 2 * Cfg::BYTES);
+          tma_load_2d_pair(st, &p.w, kb * 128, w_row, bar);
+          tma_load_2d_pair(st + Cfg::X_OFF, &p.x, kb * 128, x_row, bar);
+          tma_load_2d_pair(st + Cfg::SW_OFF, &p.ws, 0, ws, bar);
+          tma_load_2d_pair(st + Cfg::SX_OFF, &p.xs, 0, xs0, bar);
+          tma_load_2d_pair(st + Cfg::SX_OFF + NSF * kScaleTile, &p.xs, 0, xs0 + p.col_tiles, bar);
+          ws += NSF;
+          xs0 += NSF;
+          r.next(S);
+        }
+      }
+      if (!ok) {
+        // copies in flight land before the CTA retires; the member's count on
+        // the leader's barriers, so it waits a fixed ~1 ms instead
+        if (rank == 0) {
+          for (int j = max(0, loads - S); j < loads; ++j)
+            mbar_wait_drain(full + 8 * (j % S), (uint32_t)(j / S) & 1u);
+        } else {
+          const long long t0 = clock64();
+          while (clock64() - t0 < 2000000LL) {
+          }
+        }
+      }
+    }
+  } else if (warp == 1) {
+    if (rank == 0) {
+      const uint32_t sfw = tmem + 256, sfx = sfw + 4 * NSF;
+      const uint64_t dw0 = smem_desc_sw128(base, 16, 1024);
+      const uint64_t dx0 = smem_desc_sw128(base + Cfg::X_OFF, 16, 1024);
+      const uint64_t dsw0 = scale_desc(base + Cfg::SW_OFF), dsx0 = scale_desc(base + Cfg::SX_OFF);
+      const uint32_t peer = cluster_addr(base, 1) - base;
+      const uint32_t self = cluster_addr(base, 0) - base;
+      Ring r, d;
+      bool ok = true;
+      for (int tile = pair0; tile < p.tiles && ok; tile += pairs) {
+        ok = mbar_wait_cluster(dempty, d.phase ^ 1u, abort_flag, nullptr);
+        d.next(1);
+        for (int kb = 0; kb < p.kblocks; ++kb) {
+          ok = ok && mbar_wait(full + 8 * r.i, r.phase, abort_flag, nullptr);
+          if (!__all_sync(~0u, ok)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t at = r.i * (Cfg::STAGE >> 4);
+          const int steps = min(4, (p.k - kb * kMxBK + 63) >> 6);
+          if (elect_one()) {
+#pragma unroll
+            for (int i = 0; i < NSF; ++i) {
+              tmem_copy_scales_pair(sfw + 4 * i, dsw0 + at + i * (kScaleTile >> 4));
+              tmem_copy_scales_pair(sfx + 8 * i, dsx0 + at + i * (kScaleTile >> 4));
+              tmem_copy_scales_pair(sfx + 8 * i + 4, dsx0 + at + (NSF + i) * (kScaleTile >> 4));
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              if (j < steps) {
+                const int t = FMT == MX_MXFP4 ? j >> 1 : j;
+                const uint32_t sf = FMT == MX_MXFP4 ? 2u * (j & 1) : 0u;
+                mma_mx_pair<FMT>(tmem, dw0 + at + 2 * j, dx0 + at + 2 * j,
+                                 idesc_mx<FMT>(256, 256, sf), sfw + 4 * t, sfx + 8 * t,
+                                 (kb > 0 || j > 0) ? 1u : 0u);
+              }
+            }
+            mma_commit_pair(empty + self + 8 * r.i);
+            mma_commit_pair(empty + peer + 8 * r.i);
+          }
+          __syncwarp();
+          r.next(S);
+        }
+        if (ok && elect_one()) {
+          mma_commit_pair(dfull + self);
+          mma_commit_pair(dfull + peer);
+        }
+        __syncwarp();
+      }
+      if (elect_one()) mma_commit_pair(drain + self);
+      __syncwarp();
+      mbar_wait_drain(drain, 0);
+    }
+  } else {
+    const int half = (warp - 2) >> 2, quarter = warp & 3;
+    const uint32_t ta = tmem + ((uint32_t)(quarter * 32) << 16) + half * 128;
+    const float g = (p.gw ? *p.gw : 1.f) * (p.gx ? *p.gx : 1.f);
+    const uint32_t dempty0 = cluster_addr(dempty, 0);
+    Ring d;
+    bool ok = true;
+    for (int tile = pair0; tile < p.tiles; tile += pairs) {
+      const int tn = tile / p.tiles_m, tm = tile - tn * p.tiles_m;
+      const long long col = (long long)tn * 256 + rank * 128 + quarter * 32 + lane;
+      if (ok) ok = mbar_wait(dfull, d.phase, abort_flag, nullptr);
+      ok = __all_sync(~0u, ok);
+      d.next(1);
+      float v[128];
+      if (ok) {
+        tc_fence_after();
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          float u[32];
+          tmem_ld32(ta + 32 * j, u);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[32 * j + i] = u[i];
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(dempty0);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 128; ++i) v[i] = __int_as_float(0x7FFFFFFF);
+      }
+      if (col < p.n) {
+        const int token0 = tm * 256 + half * 128, tokens = p.m - token0;
+        T* out = reinterpret_cast<T*>(p.out) + (long long)token0 * p.n + col;
+#pragma unroll
+        for (int i = 0; i < 128; ++i) {
+          if (i < tokens) put(out, v[i] * g);
+          out += p.n;
+        }
+      }
+    }
+  }
+  __syncthreads();
+  cluster_sync();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, 512);
   }
 }
 
