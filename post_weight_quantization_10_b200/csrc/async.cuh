@@ -39,6 +39,16 @@ __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t
                : "memory");
 }
 
+__device__ __forceinline__ float ld_shared_f32(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+// To the shared memory of a CTA of the cluster.
+__device__ __forceinline__ void st_cluster_f32(uint32_t addr_cluster, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr_cluster), "f"(v) : "memory");
+}
+
 // True for one lane of the (converged) warp.  A role that issues tcgen05
 // instructions runs on its whole warp and elects a lane for the issue alone:
 // descriptors and loop state then stay in uniform registers.

@@ -25,14 +25,16 @@ struct PackedGemmArgs {
   int w_tma;           // rows of packed words start on 16 bytes: TMA brings them
   int stages, wbufs;   // ring depths: operand stages (64 of k), packed chunks
   int passes;          // groups of a chunk
+  int part_bytes;      // room for the ranks' partial tiles
 };
 
-constexpr int kPackedThreads = 512;
-
-// Thread roles, four warpgroups:
-//   0  warp 0: TMA producer, warp 1: MMA issuer
-//   1  decoders
-//   2, 3  consumers: thread = accumulator row, half of the tile's tokens each
+// Thread roles, by warpgroup:
+//   0    warp 0: TMA producer, warp 1: MMA issuer
+//   1..  DG groups of decoders, taking turns by the chunk
+//   then CG groups of consumers: thread = accumulator row, a share of the tokens
+// A chunk costs a decoder a chain of waits, loads, arithmetic, stores and a
+// fence of about 2000 cycles, the MMAs of 64 tokens 256: fewer tokens, more
+// groups.  256 tokens leave registers for one.
 // Turning codes into operands takes about as many instructions as there are
 // cycles in the MMAs that use them, so with C = 2 a cluster of two CTAs works
 // on the same 128 weight rows and two token tiles: each decodes half of the
@@ -42,7 +44,15 @@ constexpr int kPackedThreads = 512;
 // order through distributed shared memory.
 template <int TN, int C>
 struct PackedCfg {
-  static constexpr int HALF = TN / 2;
+  static constexpr int CG = 2, DG = TN == 64 ? 3 : TN == 128 ? 2 : 1;
+  // registers of a thread of each role; together no more than the launch's
+  // (warpgroups x 80, 96 or 128)
+  static constexpr int REGS0 = 40, REGS_D = TN == 256 ? 88 : 80,
+                       REGS_C = TN == 64 ? 96 : TN == 128 ? 136 : 192;
+  static constexpr int LAUNCH = 65536 / (128 * (1 + DG + CG)) / 8 * 8;
+  static_assert(REGS0 + DG * REGS_D + CG * REGS_C <= (1 + DG + CG) * LAUNCH, "register split");
+  static constexpr int THREADS = 128 * (1 + DG + CG);
+  static constexpr int SHARE = TN / CG;        // tokens of a consumer group
   static constexpr int X_BYTES = TN * 128, A_BYTES = 128 * 128, STAGE = X_BYTES + A_BYTES;
   static constexpr int TMEM_COLS = 2 * TN;
   static constexpr int ROWS = 128 / C;         // weight rows that a CTA decodes
@@ -179,21 +189,23 @@ __device__ __forceinline__ void put(float* p, float v) { *p = v; }
 __device__ __forceinline__ void put(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 __device__ __forceinline__ void put(__half* p, float v) { *p = __float2half_rn(v); }
 
-// Column `col` of the output, tokens token0 .. + HALF - 1.
-template <int HALF, typename T>
+// Column `col` of the output, tokens token0 .. + SHARE - 1.
+template <int SHARE, typename T>
 __device__ __forceinline__ void store_column(T* out, const PackedArgs& p, int token0, long long col,
-                                             const float2 (&acc)[HALF / 2]) {
+                                             const float2 (&acc)[SHARE / 2]) {
   T* at = out + (long long)token0 * p.n + col;
   const int tokens = p.m - token0;
 #pragma unroll
-  for (int i = 0; i < HALF; ++i) {
+  for (int i = 0; i < SHARE; ++i) {
     if (i < tokens) put(at, i & 1 ? acc[i / 2].y : acc[i / 2].x);
     at += p.n;
   }
 }
 
-template <typename X, int TN, int C>
-__global__ void __launch_bounds__(kPackedThreads, 1)
+// BITS: of a code, or 0 for p.bits (the largest tiles, which gain nothing from
+// a kernel of their own for each width; at 33 tokens it saves a fifth).
+template <typename X, int TN, int C, int BITS>
+__global__ void __launch_bounds__(PackedCfg<TN, C>::THREADS, 1)
     k_packed_gemm(const __grid_constant__ PackedGemmArgs a) {
   using Cfg = PackedCfg<TN, C>;
   const PackedArgs& p = a.p;
@@ -202,8 +214,11 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   const int S = a.stages, NW = a.wbufs, wbytes = 16 * Cfg::ROWS * p.bits;
   uint8_t* wring = smem + S * Cfg::STAGE;
-  const PackedBars bars(smem_u32(wring + NW * wbytes), S, NW);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(wring + NW * wbytes + (bars.end - bars.full_x));
+  // C = 1: partial tiles of the cluster's ranks, behind the rings
+  const uint32_t part = smem_u32(wring + NW * wbytes);
+  const PackedBars bars(part + a.part_bytes, S, NW);
+  uint32_t* tmem_slot =
+      reinterpret_cast<uint32_t*>(wring + NW * wbytes + a.part_bytes + (bars.end - bars.full_x));
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -227,7 +242,7 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(bars.rfull + 8 * i, 1);
-      mbar_init(bars.rempty + 8 * i, 8);
+      mbar_init(bars.rempty + 8 * i, 4 * Cfg::CG);
     }
     mbar_init(bars.drain, 1);
     *abort_flag = 0;
@@ -235,13 +250,16 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
   }
   if (warp == 1) tmem_alloc(smem_u32(tmem_slot), Cfg::TMEM_COLS);
   __syncthreads();
-  if (C > 1) cluster_sync();  // the peers' barriers exist
+  if (C > 1)
+    cluster_sync();  // the peers' barriers exist
+  else if (ranks > 1)
+    asm volatile("barrier.cluster.arrive.release;" ::: "memory");  // awaited before anything remote
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const int wg = warp >> 2;
 
   if (wg == 0) {
-    if constexpr (TN == 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Cfg::REGS0));
     if (warp == 0 && lane == 0) {
       // ---------------------------------------------------------- producer
       bool ok = true;
@@ -291,21 +309,25 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
       __syncwarp();
       mbar_wait_drain(bars.drain, 0);
     }
-  } else if (wg == 1) {
+  } else if (wg <= Cfg::DG) {
     // -------------------------------------------------------------- decoders
-    if constexpr (TN == 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    if constexpr (Cfg::REGS_D < Cfg::LAUNCH)
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Cfg::REGS_D));
     // The codes are decoded into registers while the MMAs still read the stage
     // that they will go to; what is left once it is free are the stores.
     Ring st, wr;
     bool ok = true;
+    int turn = Cfg::DG - wg;  // chunks until this group's next one
     const int q = lane >> 3;
-    const int row = (warp - 4) * Cfg::STEPS * 8 + (lane & 7);  // of the part decoded here
+    const int row = (warp & 3) * Cfg::STEPS * 8 + (lane & 7);  // of the part decoded here
     const int group_shift = __ffs(p.group) - 1;
     uint32_t to[4];  // of this lane's four 16-byte pieces in a stage's operand tile
 #pragma unroll
     for (int c = 0; c < 4; ++c)
       to[c] = smem_u32(smem) + Cfg::X_BYTES + (part0 + row) * 128 +
               ((((q & 1) * 4 + c) ^ (row & 7)) << 4);
+    // C > 1: the other CTA's shared memory, as seen from here
+    const uint32_t peer = C > 1 ? cluster_addr(smem_u32(smem), rank ^ 1) - smem_u32(smem) : 0u;
     for (int tile = tile0; tile < a.tiles && ok; tile += tile_step) {
       const long long row0 = (long long)(tile / a.tiles_m) * 128 + part0;
       const float* zeros = p.zero + (row0 + row) * p.groups;
@@ -317,25 +339,31 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
           next[i] = load_ahead(zeros + 8 * i * p.groups + (k >> group_shift),
                                row0 + row + 8 * i < p.n && k < p.k);
       };
-      load_zeros(ch0);
+      load_zeros(ch0 + turn);
       for (int ch = ch0; ch < ch1; ++ch) {
+        const Ring st0 = st, w = wr;
+        Ring st1 = st;
+        st1.next(S);
+        st = st1;
+        st.next(S);
+        wr.next(NW);
+        if (Cfg::DG > 1 && turn-- > 0) continue;
+        turn = Cfg::DG - 1;
 #pragma unroll
         for (int i = 0; i < Cfg::STEPS; ++i) zero[i] = next[i];
-        if (ch + 1 < ch1) load_zeros(ch + 1);
-        if (a.w_tma && !mbar_wait(bars.wfull + 8 * wr.i, wr.phase, abort_flag, nullptr)) {
+        load_zeros(ch + Cfg::DG);
+        if (a.w_tma && !mbar_wait(bars.wfull + 8 * w.i, w.phase, abort_flag, nullptr)) {
           ok = false;
           break;
         }
-        const uint8_t* buf = wring + wr.i * wbytes;
-        Ring st1 = st;
-        st1.next(S);
-        const Ring mine = q < 2 ? st : st1;  // units 0, 1 go to the first stage, 2, 3 to the second
+        const uint8_t* buf = wring + w.i * wbytes;
+        const Ring mine = q < 2 ? st0 : st1;  // units 0, 1 go to the first stage, 2, 3 to the second
         const uint32_t stage = mine.i * Cfg::STAGE;
 #pragma unroll
         for (int i = 0; i < Cfg::STEPS; i += 2) {
           uint32_t v[2][16];
           const float* z = zero + i;
-          switch (p.bits) {
+          switch (BITS ? BITS : p.bits) {
             case 1: decode_chunk<X, 1>(a, buf, row + 8 * i, q, row0, ch, z, v); break;
             case 2: decode_chunk<X, 2>(a, buf, row + 8 * i, q, row0, ch, z, v); break;
             case 3: decode_chunk<X, 3>(a, buf, row + 8 * i, q, row0, ch, z, v); break;
@@ -363,44 +391,38 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
         // the MMA and the copies read what these stores wrote through the async proxy
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
-        if (lane == 0) {
-          if (a.w_tma) mbar_arrive(bars.wempty + 8 * wr.i);
+        if (lane < 2) {  // a lane for each of the two stages
+          const uint32_t i = lane ? st1.i : st0.i, bar = bars.full_a + 8 * i;
           if (C == 1) {
-            mbar_arrive(bars.full_a + 8 * st.i);
-            mbar_arrive(bars.full_a + 8 * st1.i);
+            mbar_arrive(bar);
           } else {
             // this warp's rows to the other CTA, the other CTA's expected here
             constexpr uint32_t BYTES = Cfg::STEPS * 8 * 128;
-            const uint32_t src = smem_u32(smem) + Cfg::X_BYTES + (part0 + (warp - 4) * Cfg::STEPS * 8) * 128;
-            const uint32_t peer = rank ^ 1;
-            mbar_arrive_expect_tx(bars.full_a + 8 * st.i, BYTES);
-            mbar_arrive_expect_tx(bars.full_a + 8 * st1.i, BYTES);
-            bulk_copy_to_peer(cluster_addr(src + st.i * Cfg::STAGE, peer), src + st.i * Cfg::STAGE,
-                              BYTES, cluster_addr(bars.full_a + 8 * st.i, peer));
-            bulk_copy_to_peer(cluster_addr(src + st1.i * Cfg::STAGE, peer), src + st1.i * Cfg::STAGE,
-                              BYTES, cluster_addr(bars.full_a + 8 * st1.i, peer));
+            const uint32_t src = smem_u32(smem) + i * Cfg::STAGE + Cfg::X_BYTES +
+                                 (part0 + (warp & 3) * Cfg::STEPS * 8) * 128;
+            bulk_copy_to_peer(src + peer, src, BYTES, bar + peer);
+            mbar_arrive_expect_tx(bar, BYTES);
           }
+        } else if (lane == 2 && a.w_tma) {
+          mbar_arrive(bars.wempty + 8 * w.i);
         }
-        wr.next(NW);
-        st = st1;
-        st.next(S);
       }
     }
   } else {
     // ------------------------------------------------------------- consumers
-    if constexpr (TN == 256) asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
-    constexpr int HALF = Cfg::HALF;
-    const int half = wg - 2;
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Cfg::REGS_C));
+    constexpr int SHARE = Cfg::SHARE;
+    const int share = wg - 1 - Cfg::DG;
     const int row = (warp & 3) * 32 + lane;
-    const uint32_t ta = tmem + ((uint32_t)((warp & 3) * 32) << 16) + half * HALF;
+    const uint32_t ta = tmem + ((uint32_t)((warp & 3) * 32) << 16) + share * SHARE;
     bool ok = true;
     Ring slot;
     for (int tile = tile0; tile < a.tiles; tile += tile_step) {
       const int tn = tile / a.tiles_m, tm = (tile - tn * a.tiles_m) * C + (C > 1 ? rank : 0);
       const long long col = (long long)tn * 128 + row;
-      float2 acc[HALF / 2];
+      float2 acc[SHARE / 2];
 #pragma unroll
-      for (int i = 0; i < HALF / 2; ++i) acc[i] = make_float2(0.f, 0.f);
+      for (int i = 0; i < SHARE / 2; ++i) acc[i] = make_float2(0.f, 0.f);
       const int g0 = ch0 * a.passes, g1 = min(ch1 * a.passes, p.groups);
       const float* scale = p.scale + col * p.groups;
       float s = load_ahead(scale + g0, col < p.n && g0 < g1);
@@ -414,7 +436,7 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
         if (!ok) break;
         tc_fence_after();
 #pragma unroll
-        for (int j = 0; j < HALF / 16; ++j) {
+        for (int j = 0; j < SHARE / 16; ++j) {
           float v[16];
           tmem_ld16(ta + slot.i * TN + 16 * j, v);
 #pragma unroll
@@ -427,23 +449,28 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
       }
       if (!ok)
 #pragma unroll
-        for (int i = 0; i < HALF / 2; ++i)
+        for (int i = 0; i < SHARE / 2; ++i)
           acc[i] = make_float2(__int_as_float(0x7FFFFFFF), __int_as_float(0x7FFFFFFF));
       if (C > 1 || ranks == 1) {
-        const int token0 = tm * TN + half * HALF;
+        const int token0 = tm * TN + share * SHARE;
         if (col < p.n) {
           if (p.out_dtype == ADMMQ_DTYPE_F32)
-            store_column<HALF>((float*)p.out, p, token0, col, acc);
+            store_column<SHARE>((float*)p.out, p, token0, col, acc);
           else if (p.out_dtype == ADMMQ_DTYPE_BF16)
-            store_column<HALF>((__nv_bfloat16*)p.out, p, token0, col, acc);
+            store_column<SHARE>((__nv_bfloat16*)p.out, p, token0, col, acc);
           else
-            store_column<HALF>((__half*)p.out, p, token0, col, acc);
+            store_column<SHARE>((__half*)p.out, p, token0, col, acc);
         }
       } else {
-        float* part = reinterpret_cast<float*>(smem);  // [TN][128], over the used stages
+        // to the rank that sums these tokens: slots [rank][TN / ranks][128]
+        asm volatile("barrier.cluster.wait.acquire;" ::: "memory");  // every rank has begun
+        const int per = (TN + ranks - 1) / ranks;
 #pragma unroll
-        for (int i = 0; i < HALF; ++i)
-          part[(half * HALF + i) * 128 + row] = i & 1 ? acc[i / 2].y : acc[i / 2].x;
+        for (int i = 0; i < SHARE; ++i) {
+          const int token = share * SHARE + i, owner = token / per;
+          st_cluster_f32(cluster_addr(part + ((rank * per + token - owner * per) * 128 + row) * 4, owner),
+                         i & 1 ? acc[i / 2].y : acc[i / 2].x);
+        }
       }
     }
   }
@@ -451,20 +478,19 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
   if (C > 1) {
     cluster_sync();  // no copy or arrival from here is under way to the other CTA
   } else if (ranks > 1) {
-    cluster_sync();
-    const int row = threadIdx.x & 127;
+    if (wg <= Cfg::DG) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+    __syncwarp();
+    cluster_sync();  // all partial tiles have arrived
+    const int per = (TN + ranks - 1) / ranks, row = threadIdx.x & 127;
     const long long col = (long long)(tile0 / a.tiles_m) * 128 + row;
-    const int token0 = tile0 % a.tiles_m * TN;
-    const float* part = reinterpret_cast<const float*>(smem);
+    const int token0 = tile0 % a.tiles_m * TN + rank * per;
     if (col < p.n)
-      for (int c = rank + ranks * (threadIdx.x >> 7); c < TN && token0 + c < p.m;
-           c += ranks * (kPackedThreads / 128)) {
+      for (int c = threadIdx.x >> 7; c < per && rank * per + c < TN && token0 + c < p.m;
+           c += Cfg::THREADS / 128) {
         float v = 0.f;
-        for (uint32_t r = 0; r < ranks; ++r)
-          v += ld_cluster_f32(cluster_addr(smem_u32(part + c * 128 + row), r));
+        for (uint32_t r = 0; r < ranks; ++r) v += ld_shared_f32(part + ((r * per + c) * 128 + row) * 4);
         put_out(p, (long long)(token0 + c) * p.n + col, v);
       }
-    cluster_sync();
   }
   __syncthreads();
   if (warp == 1) {
