@@ -29,7 +29,7 @@ struct PackedGemmArgs {
 };
 
 // Thread roles, by warpgroup:
-//   0    warp 0: TMA producer, warp 1: MMA issuer
+//   0    warps 0 and 2: TMA producers, warp 1: MMA issuer
 //   1..  DG groups of decoders, taking turns by the chunk
 //   then CG groups of consumers: thread = accumulator row, a share of the tokens
 // A chunk costs a decoder a chain of waits, loads, arithmetic, stores and a
@@ -261,44 +261,46 @@ __global__ void __launch_bounds__(PackedCfg<TN, C>::THREADS, 1)
   if (wg == 0) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Cfg::REGS0));
     if (warp == 0 && lane == 0) {
-      // ---------------------------------------------------------- producer
+      // ----------------------------------------------- activations' producer
       bool ok = true;
-      Ring x, w;  // a fresh ring's buffers count as emptied once: parity 1
-      int loads = 0, chunks = 0;
+      Ring x;  // a fresh ring's buffers count as emptied once: parity 1
+      int loads = 0;
       for (int tile = tile0; tile < a.tiles && ok; tile += tile_step) {
         const int tn = tile / a.tiles_m, tm = (tile - tn * a.tiles_m) * C + (C > 1 ? rank : 0);
-        for (int ch = ch0; ch < ch1 && ok; ++ch) {
-          if (a.w_tma) {
-            const uint32_t bar = bars.wfull + 8 * w.i;
-            if (!mbar_wait(bars.wempty + 8 * w.i, w.phase ^ 1u, abort_flag, nullptr)) {
-              ok = false;
-              break;
-            }
-            mbar_arrive_expect_tx(bar, wbytes);
-            tma_load_2d(smem_u32(wring + w.i * wbytes), &a.w, ch * 16 * p.bits, tn * 128 + part0, bar);
-            w.next(NW);
-            ++chunks;
+        for (int k = ch0 * 128; k < ch1 * 128; k += 64, ++loads) {
+          const uint32_t bar = bars.full_x + 8 * x.i;
+          if (!mbar_wait(bars.empty + 8 * x.i, x.phase ^ 1u, abort_flag, nullptr)) {
+            ok = false;
+            break;
           }
-          for (int h = 0; h < 2; ++h) {
-            const uint32_t bar = bars.full_x + 8 * x.i;
-            if (!mbar_wait(bars.empty + 8 * x.i, x.phase ^ 1u, abort_flag, nullptr)) {
-              ok = false;
-              break;
-            }
-            mbar_arrive_expect_tx(bar, Cfg::X_BYTES);
-            tma_load_2d(smem_u32(smem + x.i * Cfg::STAGE), &a.x, ch * 128 + 64 * h, tm * TN, bar);
-            x.next(S);
-            ++loads;
-          }
+          mbar_arrive_expect_tx(bar, Cfg::X_BYTES);
+          tma_load_2d(smem_u32(smem + x.i * Cfg::STAGE), &a.x, k, tm * TN, bar);
+          x.next(S);
         }
       }
-      if (!ok) {
-        // the copies in flight land before the block retires
+      if (!ok)  // the copies in flight land before the block retires
         for (int j = max(0, loads - S); j < loads; ++j)
           mbar_wait_drain(bars.full_x + 8 * (j % S), (uint32_t)(j / S) & 1u);
+    } else if (warp == 2 && lane == 0 && a.w_tma) {
+      // ----------------------------------------------- packed codes' producer
+      bool ok = true;
+      Ring w;
+      int chunks = 0;
+      for (int tile = tile0; tile < a.tiles && ok; tile += tile_step)
+        for (int ch = ch0; ch < ch1; ++ch, ++chunks) {
+          const uint32_t bar = bars.wfull + 8 * w.i;
+          if (!mbar_wait(bars.wempty + 8 * w.i, w.phase ^ 1u, abort_flag, nullptr)) {
+            ok = false;
+            break;
+          }
+          mbar_arrive_expect_tx(bar, wbytes);
+          tma_load_2d(smem_u32(wring + w.i * wbytes), &a.w, ch * 16 * p.bits,
+                      tile / a.tiles_m * 128 + part0, bar);
+          w.next(NW);
+        }
+      if (!ok)
         for (int j = max(0, chunks - NW); j < chunks; ++j)
           mbar_wait_drain(bars.wfull + 8 * (j % NW), (uint32_t)(j / NW) & 1u);
-      }
     } else if (warp == 1) {
       // -------------------------------------------------------- MMA issuer
       const bool ok = a.passes == 1   ? issue_mmas<X, TN, C, 1>(a, ch0, ch1, tile0, tile_step, tmem, smem, bars, abort_flag)

@@ -51,19 +51,31 @@ int launch_gemm(const PackedArgs& p, cudaStream_t st) {
   a.w_tma = p.words % 4 == 0;
   int ranks = C;
   if (C == 1)
-    while (ranks < 8 && a.chunks >= 4 * ranks && tiles * 2 * ranks <= num_sms()) ranks *= 2;
+    while (ranks < 8 && a.chunks >= 4 * ranks && 2 * ranks * tiles <= cluster_ctas(2 * ranks)) ranks *= 2;
+  // Shared memory: the ranks' partial tiles; packed chunks, which come from HBM,
+  // a long way off (a third of the rings, at most 16); operand stages the rest.
+  // A decoder group may wait for a buffer that others have yet to use once:
+  // with a buffer for each group no wait is more than one use ahead, which is
+  // as far as a barrier's parity tells uses apart.
+  const int wbytes = 16 * Cfg::ROWS * p.bits;
+  constexpr int least_w = Cfg::DG < 2 ? 2 : Cfg::DG, least_s = 2 * (Cfg::DG < 2 ? 2 : Cfg::DG);
+  for (;; ranks /= 2) {
+    a.part_bytes = C == 1 && ranks > 1 ? ranks * cdiv(TN, ranks) * 512 : 0;
+    const int room = 225 * 1024 - a.part_bytes;
+    a.wbufs = room / 3 / wbytes;
+    a.wbufs = a.wbufs < least_w ? least_w : a.wbufs > 16 ? 16 : a.wbufs;
+    a.stages = (room - a.wbufs * wbytes) / Cfg::STAGE & ~1;
+    if (a.stages < least_s) a.stages = least_s;
+    if (a.stages > 8) a.stages = 8;
+    a.wbufs = (room - a.stages * Cfg::STAGE) / wbytes;
+    if (a.wbufs > 16) a.wbufs = 16;
+    if (a.wbufs >= least_w) break;
+    if (ranks == C) return ADMMQ_ERR_UNSUPPORTED;
+  }
   a.range = C == 1 ? cdiv(a.chunks, ranks) : a.chunks;
-  a.part_bytes = C == 1 && ranks > 1 ? ranks * cdiv(TN, ranks) * 512 : 0;
-  // four packed chunks where they fit, the rest (an even number) to operand stages
-  const int wbytes = 16 * Cfg::ROWS * p.bits, room = 225 * 1024 - a.part_bytes;
-  a.stages = (room - 4 * wbytes) / Cfg::STAGE & ~1;
-  if (a.stages < 4) a.stages = 4;
-  if (a.stages > 8) a.stages = 8;
-  a.wbufs = (room - a.stages * Cfg::STAGE) / wbytes;
-  if (a.wbufs > 4) a.wbufs = 4;
   if (!make_x_map(&a.x, p, __is_same(X, __nv_bfloat16), TN)) return ADMMQ_ERR_CUDA;
   if (a.w_tma && !make_w_map(&a.w, p, Cfg::ROWS)) return ADMMQ_ERR_CUDA;
-  int smem = a.stages * Cfg::STAGE + a.wbufs * wbytes + a.part_bytes + 1024 + 512;
+  int smem = a.stages * Cfg::STAGE + a.wbufs * wbytes + a.part_bytes + 2048;
   smem = tmem_fair_smem(smem, Cfg::TMEM_COLS);
   const void* kern;
   if constexpr (BY_BITS) {

@@ -1,8 +1,15 @@
-// tmem_fair.cuh -- how much shared memory a kernel that allocates tensor
-// memory asks for.
+// tmem_fair.cuh -- how many CTAs of a kernel that allocates tensor memory run at
+// once, and how much shared memory such a kernel asks for.
 #pragma once
+#include "host.cuh"
 
 namespace admmq {
+
+// CTAs that run at once, one per SM, in clusters of a power of two.  Clusters do
+// not straddle the GPU's processing clusters, whose sizes leave some SMs over:
+// 48 clusters of three (144 CTAs) took two rounds where 48 pairs took one, and
+// 32 clusters of four are the most that run together.
+inline int cluster_ctas(int size) { return size <= 2 ? num_sms() / size * size : 128; }
 
 // Shared memory to ask for, so that blocks which fit an SM together never ask
 // for more than its 512 tensor-memory columns: the CTAs of a cluster wait for
