@@ -24,6 +24,7 @@ DTYPE_F32, DTYPE_BF16, DTYPE_F16 = 0, 1, 2
 DTYPES = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_F16}
 MX_FORMATS = {"mxfp4": 0, "nvfp4": 1}
 MX_BLOCK = {"mxfp4": 32, "nvfp4": 16}
+_ACT_DTYPES = (torch.bfloat16, torch.float16)
 BUFFERS = ["sigma", "rsig", "hdiag", "lambda", "V", "C0", "P_hi", "P_lo", "T_hi", "T_lo",
            "E_hi", "E_lo", "Ht", "status", "row_in", "row_out"]
 ERR_INVALID_ARG, ERR_TIMEOUT, ERR_RANGE = -1, -6, -9
@@ -131,6 +132,9 @@ def lib():
         "admmq_mx_scale_bytes": (_sz, [_i64, _i, _i]),
         "admmq_mx_quantize": (_i, [_vp, _i, _i64, _i, _i64, _i, _vp, _vp, _vp, _vp]),
         "admmq_mx_dequantize": (_i, [_vp, _vp, _i64, _i, _i, _vp, _vp, _i, _i64, _vp]),
+        "admmq_mx_linear_workspace_bytes": (_sz, [_i64, _i, _i]),
+        "admmq_mx_linear": (_i, [_vp, _i, _i64, _i64, _vp, _vp, _vp, _vp, _i, _i, _i, _vp, _i, _vp,
+                                 _sz, _vp]),
         "admmq_mx_matmul": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _i64, _i, _i, _i, _vp, _i, _vp]),
     }
     for name, (res, args) in sig.items():
@@ -344,9 +348,8 @@ def pack(codes: torch.Tensor, bits: int, out: torch.Tensor | None = None, stream
     return out
 
 
-def _require(ok: bool, what: str):
-    if not ok:
-        raise AdmmqError(ERR_INVALID_ARG, what)
+def _invalid(what: str):
+    raise AdmmqError(ERR_INVALID_ARG, what)
 
 
 def _is_matrix(x: torch.Tensor, dtypes) -> bool:
@@ -358,14 +361,20 @@ def _row_stride(x: torch.Tensor) -> int:
     return x.stride(0) if x.shape[0] > 1 else x.shape[1]
 
 
+# The raw handle of a device's current stream: on the decode path a call's host
+# time counts, and a Stream object costs more than the launch.
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(
+    torch._C, "_cuda_getCurrentRawStream") else lambda i: torch.cuda.current_stream(i).cuda_stream
+
+
 def _launch(name: str, device: torch.device, stream, *args):
     """Call entry point `name` with `device` current, on `stream` (None: the
     device's current stream)."""
     if device.index != torch.cuda.current_device():
         with torch.cuda.device(device):
             return _launch(name, device, stream, *args)
-    s = stream if stream is not None else torch.cuda.current_stream()
-    rc = getattr(lib(), name)(*args, s.cuda_stream)
+    rc = getattr(_lib or lib(), name)(
+        *args, _raw_stream(device.index) if stream is None else stream.cuda_stream)
     if rc != OK:
         raise AdmmqError(rc, name)
 
@@ -382,8 +391,9 @@ def _output(out, shape, dtype, x: torch.Tensor, stream, where: str):
     """`out` after a check of its shape, type, device and layout, or a new tensor."""
     if out is None:
         return _empty(shape, dtype, x.device, stream)
-    _require(out.shape == shape and out.dtype == dtype and out.device == x.device
-             and out.is_contiguous(), f"{where}: out")
+    if not (out.shape == shape and out.dtype == dtype and out.device == x.device
+            and out.is_contiguous()):
+        _invalid(f"{where}: out")
     return out
 
 
@@ -393,21 +403,26 @@ def packed_matmul(x: torch.Tensor, packed: torch.Tensor, scale: torch.Tensor, ze
     """x [m][d_in] (bf16 or fp16) times the layer whose codes `pack` packed:
     sum over groups of scale * (code - zero) . x, [m][d_out] in `dtype`
     (x's by default).  The group size is d_in / scale.shape[1]."""
-    _require(_is_matrix(x, (torch.bfloat16, torch.float16)), "packed_matmul: x")
+    if not _is_matrix(x, _ACT_DTYPES):
+        _invalid("packed_matmul: x")
     m, d = x.shape
-    _require(packed.dim() == 2 and packed.dtype == torch.int32 and packed.is_contiguous()
-             and packed.shape[1] * 32 == d * bits and packed.device == x.device,
-             "packed_matmul: packed")
+    device = x.device
+    if not (packed.dim() == 2 and packed.dtype == torch.int32 and packed.is_contiguous()
+            and packed.shape[1] * 32 == d * bits and packed.device == device):
+        _invalid("packed_matmul: packed")
     n = packed.shape[0]
-    for name, t in (("scale", scale), ("zero", zero)):
-        _require(t.dtype == torch.float32 and t.dim() == 2 and t.shape[0] == n
-                 and t.is_contiguous() and t.device == x.device, f"packed_matmul: {name}")
+    if not (scale.dtype == torch.float32 and zero.dtype == torch.float32 and scale.dim() == 2
+            and scale.shape == zero.shape and scale.shape[0] == n and scale.is_contiguous()
+            and zero.is_contiguous() and scale.device == device and zero.device == device):
+        _invalid("packed_matmul: scale and zero")
     groups = scale.shape[1]
-    _require(zero.shape[1] == groups and groups > 0 and d % groups == 0, "packed_matmul: groups")
+    if groups < 1 or d % groups:
+        _invalid("packed_matmul: groups")
     dtype = dtype or x.dtype
-    _require(dtype in DTYPES, "packed_matmul: dtype")
+    if dtype not in DTYPES:
+        _invalid("packed_matmul: dtype")
     out = _output(out, (m, n), dtype, x, stream, "packed_matmul")
-    _launch("admmq_packed_matmul", x.device, stream, x.data_ptr(), DTYPES[x.dtype], m,
+    _launch("admmq_packed_matmul", device, stream, x.data_ptr(), DTYPES[x.dtype], m,
             _row_stride(x), packed.data_ptr(), scale.data_ptr(), zero.data_ptr(), d, n, bits,
             d // groups, out.data_ptr(), DTYPES[dtype])
     return out
@@ -428,13 +443,23 @@ class MxTensor:
     tensor_scale: torch.Tensor | None = None
 
     def __post_init__(self):
-        c, s, g = self.codes, self.scale, self.tensor_scale
-        _require(self.fmt in MX_FORMATS, "MxTensor: fmt")
-        _require(c.is_cuda and c.dtype == torch.uint8 and c.dim() == 2 and c.is_contiguous()
-                 and c.shape[1] > 0 and c.shape[1] % 16 == 0, "MxTensor: codes")
-        _require(s.dtype == torch.uint8 and s.device == c.device and s.is_contiguous()
-                 and s.numel() == _mx_scale_numel(self.rows, self.k, self.fmt), "MxTensor: scale")
-        _check_tensor_scale(g, self.fmt, c.device, "MxTensor")
+        c, s = self.codes, self.scale
+        if self.fmt not in MX_FORMATS:
+            _invalid("MxTensor: fmt")
+        if not (c.is_cuda and c.dtype == torch.uint8 and c.dim() == 2 and c.is_contiguous()
+                and c.shape[1] > 0 and c.shape[1] % 16 == 0):
+            _invalid("MxTensor: codes")
+        if not (s.dtype == torch.uint8 and s.device == c.device and s.is_contiguous()
+                and s.numel() == _mx_scale_numel(c.shape[0], 2 * c.shape[1], self.fmt)):
+            _invalid("MxTensor: scale")
+        _check_tensor_scale(self.tensor_scale, self.fmt, c.device, "MxTensor")
+
+    @classmethod
+    def _of(cls, codes, scale, fmt, tensor_scale):
+        """One that the library made itself."""
+        q = cls.__new__(cls)
+        q.__dict__.update(codes=codes, scale=scale, fmt=fmt, tensor_scale=tensor_scale)
+        return q
 
     @property
     def rows(self) -> int:
@@ -458,9 +483,23 @@ def _mx_scale_numel(rows: int, k: int, fmt: str) -> int:
 
 
 def _check_tensor_scale(g, fmt: str, device, where: str):
-    if g is not None:
-        _require(fmt == "nvfp4" and g.dtype == torch.float32 and g.numel() == 1
-                 and g.device == device, f"{where}: tensor_scale")
+    if g is not None and not (fmt == "nvfp4" and g.dtype == torch.float32 and g.numel() == 1
+                              and g.device == device):
+        _invalid(f"{where}: tensor_scale")
+
+
+def _check_mx_input(x: torch.Tensor, fmt: str, tensor_scale, where: str):
+    if not _is_matrix(x, DTYPES):
+        _invalid(f"{where}: x")
+    if fmt not in MX_FORMATS:
+        _invalid(f"{where}: fmt")
+    _check_tensor_scale(tensor_scale, fmt, x.device, where)
+    if x.shape[1] == 0 or x.shape[1] % 32:
+        _invalid(f"{where}: k is a positive multiple of 32")
+
+
+def _ptr_or_null(t):
+    return None if t is None else t.data_ptr()
 
 
 def mx_quantize(x: torch.Tensor, fmt: str = "mxfp4", tensor_scale: torch.Tensor | None = None,
@@ -469,36 +508,43 @@ def mx_quantize(x: torch.Tensor, fmt: str = "mxfp4", tensor_scale: torch.Tensor 
     microscaled 4-bit format: "mxfp4" (blocks of 32, power-of-two scales) or
     "nvfp4" (blocks of 16, e4m3 scales on top of `tensor_scale`, usually
     amax(x) / (448 * 6), fp32 [1] on the device)."""
-    _require(_is_matrix(x, DTYPES), "mx_quantize: x")
-    _require(fmt in MX_FORMATS, "mx_quantize: fmt")
-    _check_tensor_scale(tensor_scale, fmt, x.device, "mx_quantize")
+    _check_mx_input(x, fmt, tensor_scale, "mx_quantize")
     rows, k = x.shape
-    _require(k > 0 and k % 32 == 0, "mx_quantize: k is a positive multiple of 32")
-    codes = _empty((rows, k // 2), torch.uint8, x.device, stream)
-    scale = _empty(_mx_scale_numel(rows, k, fmt), torch.uint8, x.device, stream)
-    _launch("admmq_mx_quantize", x.device, stream, x.data_ptr(), DTYPES[x.dtype], rows, k,
-            _row_stride(x), MX_FORMATS[fmt], None if tensor_scale is None else tensor_scale.data_ptr(),
-            codes.data_ptr(), scale.data_ptr())
-    return MxTensor(codes, scale, fmt, tensor_scale)
+    device = x.device
+    codes = _empty((rows, k // 2), torch.uint8, device, stream)
+    scale = _empty((_mx_scale_numel(rows, k, fmt),), torch.uint8, device, stream)
+    _launch("admmq_mx_quantize", device, stream, x.data_ptr(), DTYPES[x.dtype], rows, k,
+            _row_stride(x), MX_FORMATS[fmt], _ptr_or_null(tensor_scale), codes.data_ptr(),
+            scale.data_ptr())
+    return MxTensor._of(codes, scale, fmt, tensor_scale)
 
 
 def mx_dequantize(q: MxTensor, dtype: torch.dtype = torch.bfloat16,
                   out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """The values of q, [rows][k] in `dtype` (fp32, bf16 or fp16)."""
-    _require(dtype in DTYPES, "mx_dequantize: dtype")
-    out = _output(out, (q.rows, q.k), dtype, q.codes, stream, "mx_dequantize")
-    codes, scale, g = q._ptrs()
-    _launch("admmq_mx_dequantize", q.device, stream, codes, scale, q.rows, q.k,
-            MX_FORMATS[q.fmt], g, out.data_ptr(), DTYPES[dtype], q.k)
+    if dtype not in DTYPES:
+        _invalid("mx_dequantize: dtype")
+    codes = q.codes
+    rows, half = codes.shape
+    out = _output(out, (rows, 2 * half), dtype, codes, stream, "mx_dequantize")
+    _launch("admmq_mx_dequantize", codes.device, stream, codes.data_ptr(), q.scale.data_ptr(), rows,
+            2 * half, MX_FORMATS[q.fmt], _ptr_or_null(q.tensor_scale), out.data_ptr(),
+            DTYPES[dtype], 2 * half)
     return out
+
+
+def _check_mx_weights(w: MxTensor, fmt: str, k: int, device, dtype, where: str):
+    if not (w.fmt == fmt and w.k == k and w.device == device):
+        _invalid(f"{where}: operands differ in format, k or device")
+    if w.rows == 0 or dtype not in DTYPES:
+        _invalid(f"{where}: no weights, or dtype")
 
 
 def mx_matmul(a: MxTensor, b: MxTensor, dtype: torch.dtype = torch.bfloat16,
               out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """a [m][k] times b [n][k] transposed (activations and nn.Linear weights,
     both in one microscaled format), [m][n] in `dtype` (fp32, bf16 or fp16)."""
-    _require(a.fmt == b.fmt and a.k == b.k and a.device == b.device, "mx_matmul: a and b differ")
-    _require(b.rows > 0 and dtype in DTYPES, "mx_matmul: b or dtype")
+    _check_mx_weights(b, a.fmt, a.k, a.device, dtype, "mx_matmul")
     out = _output(out, (a.rows, b.rows), dtype, a.codes, stream, "mx_matmul")
     _launch("admmq_mx_matmul", a.device, stream, *a._ptrs(), *b._ptrs(), a.rows, b.rows, a.k,
             MX_FORMATS[a.fmt], out.data_ptr(), DTYPES[dtype])
@@ -510,8 +556,21 @@ def mx_linear(x: torch.Tensor, w: MxTensor, dtype: torch.dtype | None = None,
               stream=None) -> torch.Tensor:
     """mx_matmul(mx_quantize(x, w.fmt, tensor_scale), w): a linear layer with
     4-bit weights whose activations are quantised on the way in."""
-    q = mx_quantize(x, w.fmt, tensor_scale, stream)
-    return mx_matmul(q, w, dtype or x.dtype, out, stream)
+    fmt = w.fmt
+    _check_mx_input(x, fmt, tensor_scale, "mx_linear")
+    m, k = x.shape
+    device = x.device
+    dtype = dtype or x.dtype
+    _check_mx_weights(w, fmt, k, device, dtype, "mx_linear")
+    n = w.codes.shape[0]
+    out = _output(out, (m, n), dtype, x, stream, "mx_linear")
+    f = MX_FORMATS[fmt]
+    need = (m * (k // 2) + 255 & ~255) + _mx_scale_numel(m, k, fmt)
+    ws = _empty((need,), torch.uint8, device, stream)
+    _launch("admmq_mx_linear", device, stream, x.data_ptr(), DTYPES[x.dtype], m, _row_stride(x),
+            _ptr_or_null(tensor_scale), *w._ptrs(), n, k, f, out.data_ptr(), DTYPES[dtype],
+            ws.data_ptr(), need)
+    return out
 
 
 def project(wtilde, V, sigma, rsig, hdiag, bits, group, grid, codes, scale, zero, P_hi, P_lo,

@@ -239,17 +239,18 @@ int launch_tile(MxArgs& p, cudaStream_t st) {
   constexpr int NSF = kMxBK / MxFormat<FMT>::TILE_K;
   const int xt = (p.tn + 127) / 128, tiles = p.tiles_n * (p.tn < 128 ? 1 : cdiv(p.m, p.tn));
   int ranks = 1;
-  while (ranks < 8 && 2 * ranks <= p.kblocks && tiles * 2 * ranks <= 2 * num_sms()) ranks *= 2;
+  while (ranks < 8 && 2 * ranks <= p.kblocks && tiles * 2 * ranks <= cluster_ctas(2 * ranks)) ranks *= 2;
   p.stage_bytes = 128 * 128 + ((p.tn * 128 + 1023) & ~1023) + (((1 + xt) * NSF * kScaleTile + 1023) & ~1023);
-  const int blocks = cdiv(p.kblocks, ranks);
-  p.stages = 200 * 1024 / p.stage_bytes;
+  p.part_bytes = ranks > 1 ? ranks * cdiv(p.tn, ranks) * 512 : 0;
+  // everything that a block reads on its way at once, or half of an SM's
+  // shared memory where the blocks are more than the SMs
+  const int blocks = cdiv(p.kblocks, ranks), room = tiles * ranks > num_sms() ? 108 * 1024 : 216 * 1024;
+  p.stages = (room - p.part_bytes) / p.stage_bytes;
   if (p.stages > blocks) p.stages = blocks;
-  p.bar_off = p.stages * p.stage_bytes;
-  if (ranks > 1 && p.bar_off < p.tn * 512) p.bar_off = p.tn * 512;
   const int cols = ((p.tn + 31) & ~31) + 4 * NSF * (1 + xt);
   p.tmem_cols = 32;
   while (p.tmem_cols < cols) p.tmem_cols *= 2;
-  const int smem = tmem_fair_smem(p.bar_off + 1024 + 16 * p.stages + 64, p.tmem_cols);
+  const int smem = tmem_fair_smem(p.stages * p.stage_bytes + p.part_bytes + 1024 + 16 * p.stages + 64, p.tmem_cols);
   auto kern = k_mx_tile<FMT, T>;
   CK(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
   cudaLaunchConfig_t lc = {};
@@ -288,6 +289,49 @@ bool dtype_ok(int dtype) { return dtype >= ADMMQ_DTYPE_F32 && dtype <= ADMMQ_DTY
   } else {                                               \
     MX_DISPATCH_T(MX_NVFP4, dtype, BODY)                 \
   }
+
+namespace {
+
+// The product of two MX matrices; check_only: its argument checks alone.
+int mx_product(const uint8_t* a_codes, const uint8_t* a_scale, const float* a_tensor_scale,
+                    const uint8_t* b_codes, const uint8_t* b_scale, const float* b_tensor_scale,
+                    int64_t m, int n, int k, int fmt, void* out, int out_dtype, void* stream, bool check_only) {
+  if (!mx_shape_ok(m, k, fmt) || !mx_shape_ok(n, k, fmt) || n < 1 || !dtype_ok(out_dtype))
+    return ADMMQ_ERR_INVALID_ARG;
+  if (fmt == ADMMQ_MX_MXFP4 && (a_tensor_scale || b_tensor_scale)) return ADMMQ_ERR_INVALID_ARG;
+  if ((((uintptr_t)a_tensor_scale | (uintptr_t)b_tensor_scale) & 3) != 0)
+    return ADMMQ_ERR_INVALID_ARG;
+  if (m == 0) return ADMMQ_OK;
+  if (!a_codes || !a_scale || !b_codes || !b_scale || !out || !aligned16(a_codes) ||
+      !aligned16(a_scale) || !aligned16(b_codes) || !aligned16(b_scale) || !aligned16(out))
+    return ADMMQ_ERR_INVALID_ARG;
+  int rc = device_ok();
+  if (rc || check_only) return rc;
+  MxArgs p;
+  p.w_scale = b_scale;
+  p.x_scale = a_scale;
+  p.gw = b_tensor_scale;
+  p.gx = a_tensor_scale;
+  p.out = out;
+  p.m = (int)m;
+  p.n = n;
+  p.k = k;
+  p.tn = m <= 128 ? ((int)m + 15) / 16 * 16 : 256;
+  p.tiles_n = cdiv(n, 128);
+  p.kblocks = cdiv(k, kMxBK);
+  p.col_tiles = cdiv(k, mx_tile_k(fmt));
+  const bool pair = m > 128;
+  if (!pair && (!make_codes_map(&p.w, b_codes, k, n, 128) || !make_codes_map(&p.x, a_codes, k, m, p.tn)))
+    return ADMMQ_ERR_CUDA;
+#define PRODUCT(FMT, T)                                                            \
+  rc = pair ? launch_pair<FMT, T>(b_codes, a_codes, p, (cudaStream_t)stream)       \
+            : launch_tile<FMT, T>(p, (cudaStream_t)stream)
+  MX_DISPATCH(fmt, out_dtype, PRODUCT)
+#undef PRODUCT
+  return rc;
+}
+
+}  // namespace
 
 extern "C" {
 
@@ -347,39 +391,34 @@ int admmq_mx_dequantize(const uint8_t* codes, const uint8_t* scale, int64_t rows
 int admmq_mx_matmul(const uint8_t* a_codes, const uint8_t* a_scale, const float* a_tensor_scale,
                     const uint8_t* b_codes, const uint8_t* b_scale, const float* b_tensor_scale,
                     int64_t m, int n, int k, int fmt, void* out, int out_dtype, void* stream) {
-  if (!mx_shape_ok(m, k, fmt) || !mx_shape_ok(n, k, fmt) || n < 1 || !dtype_ok(out_dtype))
-    return ADMMQ_ERR_INVALID_ARG;
-  if (fmt == ADMMQ_MX_MXFP4 && (a_tensor_scale || b_tensor_scale)) return ADMMQ_ERR_INVALID_ARG;
-  if ((((uintptr_t)a_tensor_scale | (uintptr_t)b_tensor_scale) & 3) != 0)
+  return mx_product(a_codes, a_scale, a_tensor_scale, b_codes, b_scale, b_tensor_scale, m, n, k, fmt,
+                    out, out_dtype, stream, false);
+}
+
+size_t admmq_mx_linear_workspace_bytes(int64_t m, int k, int fmt) {
+  if (!mx_shape_ok(m, k, fmt)) return 0;
+  return (((size_t)m * (k / 2) + 255) & ~(size_t)255) + admmq_mx_scale_bytes(m, k, fmt);
+}
+
+int admmq_mx_linear(const void* x, int x_dtype, int64_t m, int64_t ldx, const float* x_tensor_scale,
+                    const uint8_t* w_codes, const uint8_t* w_scale, const float* w_tensor_scale,
+                    int n, int k, int fmt, void* out, int out_dtype, void* ws, size_t ws_bytes,
+                    void* stream) {
+  if (!mx_shape_ok(m, k, fmt) || !dtype_ok(x_dtype) || !dtype_ok(out_dtype) || n < 1 || ldx < k)
     return ADMMQ_ERR_INVALID_ARG;
   if (m == 0) return ADMMQ_OK;
-  if (!a_codes || !a_scale || !b_codes || !b_scale || !out || !aligned16(a_codes) ||
-      !aligned16(a_scale) || !aligned16(b_codes) || !aligned16(b_scale) || !aligned16(out))
-    return ADMMQ_ERR_INVALID_ARG;
-  int rc = device_ok();
+  if (!x || !w_codes || !w_scale || !out || !ws || ((uintptr_t)ws & 255)) return ADMMQ_ERR_INVALID_ARG;
+  if (ws_bytes < admmq_mx_linear_workspace_bytes(m, k, fmt)) return ADMMQ_ERR_WORKSPACE;
+  uint8_t* codes = (uint8_t*)ws;
+  uint8_t* scale = codes + (((size_t)m * (k / 2) + 255) & ~(size_t)255);
+  // the product's arguments first: nothing is launched when they are refused
+  int rc = mx_product(codes, scale, x_tensor_scale, w_codes, w_scale, w_tensor_scale, m, n, k, fmt,
+                      out, out_dtype, stream, true);
   if (rc) return rc;
-  MxArgs p;
-  p.w_scale = b_scale;
-  p.x_scale = a_scale;
-  p.gw = b_tensor_scale;
-  p.gx = a_tensor_scale;
-  p.out = out;
-  p.m = (int)m;
-  p.n = n;
-  p.k = k;
-  p.tn = m <= 128 ? ((int)m + 15) / 16 * 16 : 256;
-  p.tiles_n = cdiv(n, 128);
-  p.kblocks = cdiv(k, kMxBK);
-  p.col_tiles = cdiv(k, mx_tile_k(fmt));
-  const bool pair = m > 128;
-  if (!pair && (!make_codes_map(&p.w, b_codes, k, n, 128) || !make_codes_map(&p.x, a_codes, k, m, p.tn)))
-    return ADMMQ_ERR_CUDA;
-#define PRODUCT(FMT, T)                                                            \
-  rc = pair ? launch_pair<FMT, T>(b_codes, a_codes, p, (cudaStream_t)stream)       \
-            : launch_tile<FMT, T>(p, (cudaStream_t)stream)
-  MX_DISPATCH(fmt, out_dtype, PRODUCT)
-#undef PRODUCT
-  return rc;
+  rc = admmq_mx_quantize(x, x_dtype, m, k, ldx, fmt, x_tensor_scale, codes, scale, stream);
+  if (rc) return rc;
+  return mx_product(codes, scale, x_tensor_scale, w_codes, w_scale, w_tensor_scale, m, n, k, fmt,
+                    out, out_dtype, stream, false);
 }
 
 }  // extern "C"

@@ -73,7 +73,7 @@ struct MxArgs {
                                // of them, or 128 or 256 (tiles start at a scale tile's row 0)
   int tiles_n;                 // 128-column tiles
   int kblocks, col_tiles;      // 256-element stages; scale tiles along k
-  int stages, stage_bytes, bar_off;
+  int stages, stage_bytes, part_bytes;  // part_bytes: the ranks' partial tiles
   int tmem_cols;
 };
 
@@ -81,8 +81,9 @@ constexpr int kMxBK = 256;  // elements of K per stage: 128-byte rows
 constexpr int kMxTileThreads = 192;
 
 // One output tile of 128 columns x tn tokens per cluster; the cluster's CTAs
-// share the reduction (contiguous ranges of stages) and add their partial
-// tiles through distributed shared memory, in rank order.
+// share the reduction (contiguous ranges of stages); each rank sums a share of
+// the tokens, from partial tiles that all ranks store into its shared memory,
+// in rank order.
 //   warp 0  TMA producer    warp 1  MMA issuer    warps 2-5  epilogue
 template <int FMT, typename T>
 __global__ void __launch_bounds__(kMxTileThreads)
@@ -95,7 +96,7 @@ __global__ void __launch_bounds__(kMxTileThreads)
   const int x_bytes = p.tn * 128;
   const int x_off = 128 * 128, sw_off = x_off + ((x_bytes + 1023) & ~1023),
             sx_off = sw_off + NSF * kScaleTile;
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + p.bar_off);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + p.stages * p.stage_bytes + p.part_bytes);
   uint64_t* empty = full + p.stages;
   uint64_t* done = empty + p.stages;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
@@ -121,6 +122,8 @@ __global__ void __launch_bounds__(kMxTileThreads)
   }
   if (warp == 1) tmem_alloc(smem_u32(tmem_slot), p.tmem_cols);
   __syncthreads();
+  // awaited before anything is stored into another rank
+  if (ranks > 1) asm volatile("barrier.cluster.arrive.release;" ::: "memory");
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
@@ -198,42 +201,53 @@ __global__ void __launch_bounds__(kMxTileThreads)
   // ------------------------------------------------------------- epilogue
   const int row = (warp & 3) * 32 + lane;  // column of the output tile
   const uint32_t ta = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-  float* part = reinterpret_cast<float*>(smem);  // [tn][128], over the drained stages
   bool ok = true;
   const long long col = (long long)tn_tile * 128 + row;
   const int tokens = min(p.tn, p.m - tm_tile * p.tn);
   const float g = (p.gw ? *p.gw : 1.f) * (p.gx ? *p.gx : 1.f);
   T* out = reinterpret_cast<T*>(p.out) + (long long)tm_tile * p.tn * p.n + col;
+  const int per = (tokens + (int)ranks - 1) / (int)ranks;  // tokens that a rank sums
+  const uint32_t part = smem_u32(smem) + p.stages * p.stage_bytes;  // [ranks][per][128]
   if (warp >= 2) {
     ok = mbar_wait(smem_u32(done), 0, abort_flag, nullptr);
     ok = __all_sync(~0u, ok) && !*abort_flag;
     tc_fence_after();
-    for (int c = 0; c < p.tn; c += 16) {
+    if (ranks > 1) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+    int owner = 0, at = 0;  // of the next token
+    for (int c = 0; c < tokens; c += 16) {
       float v[16];
       tmem_ld16(ta + c, v);
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
+        if (c + i >= tokens) break;
         if (!ok) v[i] = __int_as_float(0x7FFFFFFF);
-        if (ranks > 1)
-          part[(c + i) * 128 + row] = v[i];
-        else if (col < p.n && c + i < tokens)
+        if (ranks > 1) {
+          st_cluster_f32(cluster_addr(part + (((int)rank * per + at) * 128 + row) * 4, owner), v[i]);
+          if (++at == per) {
+            at = 0;
+            ++owner;
+          }
+        } else if (col < p.n) {
           put(out + (long long)(c + i) * p.n, v[i] * g);
+        }
       }
     }
     tc_fence_before();
+  } else if (ranks > 1) {
+    asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
   }
   if (ranks > 1) {
-    cluster_sync();
+    __syncwarp();
+    cluster_sync();  // all partial tiles have arrived
     if (warp >= 2 && col < p.n) {
-      const int c0 = (int)(rank * p.tn / ranks), c1 = min((int)((rank + 1) * p.tn / ranks), tokens);
+      const int c0 = (int)rank * per, c1 = min(c0 + per, tokens);
       for (int c = c0; c < c1; ++c) {
         float v = 0.f;
         for (uint32_t r = 0; r < ranks; ++r)
-          v += ld_cluster_f32(cluster_addr(smem_u32(part + c * 128 + row), r));
+          v += ld_shared_f32(part + (((int)r * per + c - c0) * 128 + row) * 4);
         put(out + (long long)c * p.n, v * g);
       }
     }
-    cluster_sync();
   }
   __syncthreads();
   if (warp == 1) {
