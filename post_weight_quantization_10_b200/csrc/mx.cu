@@ -9,55 +9,13 @@ using namespace admmq;
 
 namespace {
 
-// Eight consecutive elements of a row as fp32 (16 bytes of a 16-bit type, 32
-// of fp32; 16-byte aligned).
-__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
-  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-}
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8]) {
-  const uint4 a = *reinterpret_cast<const uint4*>(p);
-  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = __uint_as_float(w[i] << 16);
-    v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-  }
-}
-__device__ __forceinline__ void load8(const __half* p, float (&v)[8]) {
-  const uint4 a = *reinterpret_cast<const uint4*>(p);
-  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-    v[2 * i] = f.x;
-    v[2 * i + 1] = f.y;
-  }
-}
-__device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
-  reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-  reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
-}
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8]) {
-  __nv_bfloat162 h[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-  *reinterpret_cast<uint4*>(p) = *reinterpret_cast<uint4*>(h);
-}
-__device__ __forceinline__ void store8(__half* p, const float (&v)[8]) {
-  __half2 h[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) h[i] = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
-  *reinterpret_cast<uint4*>(p) = *reinterpret_cast<uint4*>(h);
-}
-
-// A block of threads takes 128 rows x 256 columns: the scale tiles it fills
-// (or reads) are whole and lie next to each other, 1 KB (mxfp4) or 2 KB
-// (nvfp4).  A warp takes a row at a time, a lane eight elements of it; the
-// four (two) lanes of a block find its largest magnitude by shuffles.
-constexpr int kSpan = 256;  // columns of a thread block
+// A block of threads takes 128 rows x 512 columns: the scale tiles it fills
+// (or reads) are whole and lie next to each other, 2 KB (mxfp4) or 4 KB
+// (nvfp4).  A warp takes a row at a time, a lane 16 elements of it: an nvfp4
+// block, or half of an mxfp4 one, whose two lanes share its largest magnitude.
+constexpr int kSpan = 512;  // columns of a thread block
 constexpr int kMxThreads = 256;
+constexpr int kMxRows = 128 / (kMxThreads / 32);  // rows of a warp
 
 template <int FMT, typename T>
 __global__ void __launch_bounds__(kMxThreads)
@@ -65,66 +23,63 @@ __global__ void __launch_bounds__(kMxThreads)
                   const float* __restrict__ tensor_scale, uint8_t* __restrict__ codes,
                   uint8_t* __restrict__ scale) {
   constexpr int TILE_K = MxFormat<FMT>::TILE_K;
-  constexpr int LANES = MxFormat<FMT>::BLOCK / 8;  // lanes that share a block
+  constexpr int LANES = MxFormat<FMT>::BLOCK / 16;  // lanes that share a block
   constexpr int TILES = kSpan / TILE_K;
   __shared__ __align__(16) uint8_t tile[TILES * kScaleTile];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const long long row_tile = blockIdx.x / spans;
   const int span = (int)(blockIdx.x - row_tile * spans);
-  const int col = span * kSpan + lane * 8;
+  const int col = span * kSpan + lane * 16;
   const float g = FMT == MX_NVFP4 && tensor_scale ? *tensor_scale : 1.f;
-  for (int i = threadIdx.x; i < TILES * kScaleTile / 16; i += kMxThreads)
-    reinterpret_cast<uint4*>(tile)[i] = make_uint4(0, 0, 0, 0);
+  const float r6g = 1.f / (6.f * g);
+  const int col_tiles = (k + TILE_K - 1) / TILE_K;
+  const int here = min(TILES, col_tiles - span * TILES);
+  const int last = rows - row_tile * 128 < 128 ? (int)(rows - row_tile * 128) : 128;
+  // bytes of blocks or rows that do not exist are zero
+  if (last < 128 || (k % TILE_K != 0 && here < TILES + 1))
+    for (int i = threadIdx.x; i < TILES * kScaleTile / 16; i += kMxThreads)
+      reinterpret_cast<uint4*>(tile)[i] = make_uint4(0, 0, 0, 0);
   __syncthreads();
-#pragma unroll 4
-  for (int j = 0; j < 128 / (kMxThreads / 32); ++j) {
-    const int r = j * (kMxThreads / 32) + warp;
-    const long long row = row_tile * 128 + r;
-    // all lanes stay for the shuffles; a block's lanes are valid together
-    const bool valid = row < rows && col < k;
-    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (valid) load8(x + row * ld + col, v);
-    uint32_t amax = 0;
+  const T* src = x + (row_tile * 128 + warp * kMxRows) * ld + col;
+  uint8_t* dst = codes + ((row_tile * 128 + warp * kMxRows) * k + col) / 2;
+  const int c = lane / LANES;
+  uint8_t* to = tile + (c >> 2) * kScaleTile + (c & 3);
+  const int n = min(kMxRows, last - warp * kMxRows);
+  // a block's lanes are inside or outside together; all stay for the shuffle
+  const bool in = col < k;
+  const bool wide = (((uintptr_t)x | (uintptr_t)(ld * sizeof(T))) & 31) == 0;
+  // a few rows' loads go out before the first is used (the rare exact path's
+  // branch would keep the compiler from doing so itself)
+  constexpr int AHEAD = 4;
+  for (int j0 = 0; j0 < n; j0 += AHEAD) {
+    Raw16<T> raw[AHEAD];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) amax = max(amax, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+    for (int j = 0; j < AHEAD; ++j) {
 #pragma unroll
-    for (int o = LANES / 2; o > 0; o >>= 1) amax = max(amax, __shfl_xor_sync(~0u, amax, o));
-    const uint32_t byte = block_scale<FMT>(amax, g);
-    uint32_t out = 0;
-    if (amax < 0x7F800000u) {
-      if (FMT == MX_MXFP4) {
-        const float inv = e8m0_inverse(byte);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) out |= e2m1x2(v[2 * i] * inv, v[2 * i + 1] * inv) << (8 * i);
-      } else {
-        float t = block_step<FMT>(byte, g);
-        if (t > 0.f) {
-          // tiny steps: both sides times 2^64, so that 1 / t is finite
-          const float up = t < 0x1p-64f ? 0x1p64f : 1.f;
-          t *= up;
-          const float r1 = __frcp_rn(t);
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            out |= e2m1x2(quotient_to_odd(v[2 * i] * up, t, r1),
-                          quotient_to_odd(v[2 * i + 1] * up, t, r1))
-                   << (8 * i);
-        }
-      }
+      for (int i = 0; i < (int)(4 * sizeof(T)); ++i) raw[j].w[i] = 0u;
+      if (in && j0 + j < n) load_raw(src + j * ld, wide, raw[j]);
     }
-    if (valid) {
-      *reinterpret_cast<uint32_t*>(codes + (row * k + col) / 2) = out;
-      if (lane % LANES == 0) {
-        const int c = lane / LANES;
-        tile[(c >> 2) * kScaleTile + scale_at(r, c & 3)] = (uint8_t)byte;
+    src += AHEAD * ld;
+#pragma unroll
+    for (int j = 0; j < AHEAD; ++j) {
+      if (j0 + j >= n) break;
+      float v[16];
+      values_of(raw[j], v);
+      uint32_t amax = amax_of(raw[j]);
+      if (LANES == 2) amax = max(amax, __shfl_xor_sync(~0u, amax, 1));
+      const uint32_t byte = block_scale<FMT>(amax, g, r6g);
+      const uint2 out = quantize16<FMT>(v, byte, g);
+      if (in) {
+        *reinterpret_cast<uint2*>(dst) = out;
+        if (lane % LANES == 0) to[scale_at(warp * kMxRows + j0 + j, 0)] = (uint8_t)byte;
       }
+      dst += k / 2;
     }
   }
   __syncthreads();
-  const int col_tiles = (k + TILE_K - 1) / TILE_K;
-  const int here = min(TILES, col_tiles - span * TILES);
-  uint4* dst = reinterpret_cast<uint4*>(scale + (row_tile * col_tiles + span * TILES) * kScaleTile);
+  uint4* out = reinterpret_cast<uint4*>(scale + (row_tile * col_tiles + span * TILES) * kScaleTile);
   for (int i = threadIdx.x; i < here * kScaleTile / 16; i += kMxThreads)
-    dst[i] = reinterpret_cast<const uint4*>(tile)[i];
+    out[i] = reinterpret_cast<const uint4*>(tile)[i];
 }
 
 template <int FMT, typename T>
@@ -133,38 +88,52 @@ __global__ void __launch_bounds__(kMxThreads)
                     long long rows, int k, int spans, const float* __restrict__ tensor_scale,
                     T* __restrict__ out, long long ld) {
   constexpr int TILE_K = MxFormat<FMT>::TILE_K;
-  constexpr int LANES = MxFormat<FMT>::BLOCK / 8;
+  constexpr int LANES = MxFormat<FMT>::BLOCK / 16;
   constexpr int TILES = kSpan / TILE_K;
   __shared__ __align__(16) uint8_t tile[TILES * kScaleTile];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const long long row_tile = blockIdx.x / spans;
   const int span = (int)(blockIdx.x - row_tile * spans);
-  const int col = span * kSpan + lane * 8;
+  const int col = span * kSpan + lane * 16;
   const float g = FMT == MX_NVFP4 && tensor_scale ? *tensor_scale : 1.f;
   const int col_tiles = (k + TILE_K - 1) / TILE_K;
   const int here = min(TILES, col_tiles - span * TILES);
-  const uint4* src =
+  const uint4* in =
       reinterpret_cast<const uint4*>(scale + (row_tile * col_tiles + span * TILES) * kScaleTile);
   for (int i = threadIdx.x; i < here * kScaleTile / 16; i += kMxThreads)
-    reinterpret_cast<uint4*>(tile)[i] = src[i];
+    reinterpret_cast<uint4*>(tile)[i] = __ldg(in + i);
   __syncthreads();
   if (col >= k) return;
+  const int last = rows - row_tile * 128 < 128 ? (int)(rows - row_tile * 128) : 128;
+  const int n = min(kMxRows, last - warp * kMxRows);
+  const uint8_t* src = codes + ((row_tile * 128 + warp * kMxRows) * k + col) / 2;
+  T* dst = out + (row_tile * 128 + warp * kMxRows) * ld + col;
   const int c = lane / LANES;
-#pragma unroll 8
-  for (int j = 0; j < 128 / (kMxThreads / 32); ++j) {
-    const int r = j * (kMxThreads / 32) + warp;
-    const long long row = row_tile * 128 + r;
-    if (row >= rows) break;
-    const uint32_t in = *reinterpret_cast<const uint32_t*>(codes + (row * k + col) / 2);
-    const float t = block_step<FMT>(tile[(c >> 2) * kScaleTile + scale_at(r, c & 3)], g);
-    float v[8];
+  const uint8_t* from = tile + (c >> 2) * kScaleTile + (c & 3);
+  const bool wide = (((uintptr_t)out | (uintptr_t)(ld * sizeof(T))) & 31) == 0;
+  constexpr int AHEAD = 8;
+  for (int j0 = 0; j0 < n; j0 += AHEAD) {
+    uint2 w[AHEAD];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 f = e2m1x2_values((in >> (8 * i)) & 0xFFu);
-      v[2 * i] = f.x * t;
-      v[2 * i + 1] = f.y * t;
+    for (int j = 0; j < AHEAD; ++j)
+      w[j] = j0 + j < n ? __ldg(reinterpret_cast<const uint2*>(src + (long long)j * (k / 2))) : make_uint2(0, 0);
+    src += (long long)AHEAD * (k / 2);
+#pragma unroll
+    for (int j = 0; j < AHEAD; ++j) {
+      if (j0 + j >= n) break;
+      const float t = block_step<FMT>(from[scale_at(warp * kMxRows + j0 + j, 0)], g);
+      float v[16];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float2 f = e2m1x2_values(((i < 4 ? w[j].x : w[j].y) >> (8 * (i & 3))) & 0xFFu);
+        v[2 * i] = f.x * t;
+        v[2 * i + 1] = f.y * t;
+      }
+      Raw16<T> r;
+      raw_of(v, r);
+      store_raw(dst, wide, r);
+      dst += ld;
     }
-    store8(out + row * ld + col, v);
   }
 }
 
