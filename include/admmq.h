@@ -324,11 +324,14 @@ int admmq_mx_matmul(const uint8_t* a_codes_dev, const uint8_t* a_scale_dev,
                     int k, int fmt, void* out_dev, int out_dtype, void* stream);
 
 /* A linear layer with 4-bit weights: x [m][k] (fp32, bf16 or fp16, rows ldx
- * apart, as for admmq_mx_quantize) quantised into the workspace in the weights'
- * format, then multiplied with w [n][k] as by admmq_mx_matmul (the same bits).
- *   ws_dev  at least admmq_mx_linear_workspace_bytes(m, k, fmt) bytes, 256-byte
- *           aligned; calls that overlap on the GPU need workspaces of their own. */
-size_t admmq_mx_linear_workspace_bytes(int64_t m, int k, int fmt);
+ * apart, as for admmq_mx_quantize) quantised in the weights' format (into the
+ * workspace, or inside the product for a few tokens), then multiplied with
+ * w [n][k] as by admmq_mx_matmul (the same bits).
+ *   ws_dev  at least admmq_mx_linear_workspace_bytes(m, n, k, fmt) bytes (of the
+ *           current device; 0 where none is needed: ws_dev may be NULL then),
+ *           256-byte aligned; calls that overlap on the GPU need workspaces of
+ *           their own. */
+size_t admmq_mx_linear_workspace_bytes(int64_t m, int n, int k, int fmt);
 int admmq_mx_linear(const void* x_dev, int x_dtype, int64_t m, int64_t ldx,
                     const float* x_tensor_scale_dev, const uint8_t* w_codes_dev,
                     const uint8_t* w_scale_dev, const float* w_tensor_scale_dev, int n, int k,

@@ -132,7 +132,7 @@ def lib():
         "admmq_mx_scale_bytes": (_sz, [_i64, _i, _i]),
         "admmq_mx_quantize": (_i, [_vp, _i, _i64, _i, _i64, _i, _vp, _vp, _vp, _vp]),
         "admmq_mx_dequantize": (_i, [_vp, _vp, _i64, _i, _i, _vp, _vp, _i, _i64, _vp]),
-        "admmq_mx_linear_workspace_bytes": (_sz, [_i64, _i, _i]),
+        "admmq_mx_linear_workspace_bytes": (_sz, [_i64, _i, _i, _i]),
         "admmq_mx_linear": (_i, [_vp, _i, _i64, _i64, _vp, _vp, _vp, _vp, _i, _i, _i, _vp, _i, _vp,
                                  _sz, _vp]),
         "admmq_mx_matmul": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _i64, _i, _i, _i, _vp, _i, _vp]),
@@ -565,11 +565,11 @@ def mx_linear(x: torch.Tensor, w: MxTensor, dtype: torch.dtype | None = None,
     n = w.codes.shape[0]
     out = _output(out, (m, n), dtype, x, stream, "mx_linear")
     f = MX_FORMATS[fmt]
-    need = (m * (k // 2) + 255 & ~255) + _mx_scale_numel(m, k, fmt)
-    ws = _empty((need,), torch.uint8, device, stream)
+    need = (_lib or lib()).admmq_mx_linear_workspace_bytes(m, n, k, f)
+    ws = _empty((need,), torch.uint8, device, stream) if need else None
     _launch("admmq_mx_linear", device, stream, x.data_ptr(), DTYPES[x.dtype], m, _row_stride(x),
             _ptr_or_null(tensor_scale), *w._ptrs(), n, k, f, out.data_ptr(), DTYPES[dtype],
-            ws.data_ptr(), need)
+            _ptr_or_null(ws), need)
     return out
 
 

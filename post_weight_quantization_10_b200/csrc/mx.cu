@@ -138,11 +138,11 @@ __global__ void __launch_bounds__(kMxThreads)
 }
 
 bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
+int mx_tile_k(int fmt) { return fmt == ADMMQ_MX_MXFP4 ? 128 : 64; }
 bool mx_shape_ok(int64_t rows, int k, int fmt) {
   return rows >= 0 && rows <= (1ll << 30) && k > 0 && k % 32 == 0 && k <= (1 << 24) &&
          (fmt == ADMMQ_MX_MXFP4 || fmt == ADMMQ_MX_NVFP4);
 }
-int mx_tile_k(int fmt) { return fmt == ADMMQ_MX_MXFP4 ? 128 : 64; }
 int dtype_size(int dtype) { return dtype == ADMMQ_DTYPE_F32 ? 4 : 2; }
 // Codes [rows][k / 2] in boxes of 128 bytes x box_rows, 128-byte swizzle,
 // bytes out of range read as zero (the code of 0).
@@ -203,24 +203,40 @@ int launch_pair(const uint8_t* w_codes, const uint8_t* x_codes, const MxArgs& q,
   return ADMMQ_OK;
 }
 
-template <int FMT, typename T>
-int launch_tile(MxArgs& p, cudaStream_t st) {
-  constexpr int NSF = kMxBK / MxFormat<FMT>::TILE_K;
+// How k_mx_tile's work is laid out: ranks of a cluster (returned), stages.
+// `fits`: every stage of a block is resident at once.
+int plan_tile(MxArgs& p, int fmt, bool& fits) {
+  const int nsf = kMxBK / mx_tile_k(fmt);
   const int xt = (p.tn + 127) / 128, tiles = p.tiles_n * (p.tn < 128 ? 1 : cdiv(p.m, p.tn));
   int ranks = 1;
   while (ranks < 8 && 2 * ranks <= p.kblocks && tiles * 2 * ranks <= cluster_ctas(2 * ranks)) ranks *= 2;
-  p.stage_bytes = 128 * 128 + ((p.tn * 128 + 1023) & ~1023) + (((1 + xt) * NSF * kScaleTile + 1023) & ~1023);
+  p.stage_bytes = 128 * 128 + ((p.tn * 128 + 1023) & ~1023) + (((1 + xt) * nsf * kScaleTile + 1023) & ~1023);
   p.part_bytes = ranks > 1 ? ranks * cdiv(p.tn, ranks) * 512 : 0;
   // everything that a block reads on its way at once, or half of an SM's
   // shared memory where the blocks are more than the SMs
   const int blocks = cdiv(p.kblocks, ranks), room = tiles * ranks > num_sms() ? 108 * 1024 : 216 * 1024;
   p.stages = (room - p.part_bytes) / p.stage_bytes;
-  if (p.stages > blocks) p.stages = blocks;
+  fits = p.stages >= blocks;
+  if (fits) p.stages = blocks;
+  return ranks;
+}
+
+// Tokens that k_mx_tile quantises itself, where its stages fit: every block
+// then repeats the work for its part of k, which for 16 tokens takes about as
+// long as its weights do to arrive.
+constexpr int kFusedTokens = 16;
+
+template <int FMT, typename T>
+int launch_tile(MxArgs& p, bool fused, cudaStream_t st) {
+  constexpr int NSF = kMxBK / MxFormat<FMT>::TILE_K;
+  bool fits;
+  const int ranks = plan_tile(p, FMT, fits);
+  const int xt = (p.tn + 127) / 128, tiles = p.tiles_n * (p.tn < 128 ? 1 : cdiv(p.m, p.tn));
   const int cols = ((p.tn + 31) & ~31) + 4 * NSF * (1 + xt);
   p.tmem_cols = 32;
   while (p.tmem_cols < cols) p.tmem_cols *= 2;
   const int smem = tmem_fair_smem(p.stages * p.stage_bytes + p.part_bytes + 1024 + 16 * p.stages + 64, p.tmem_cols);
-  auto kern = k_mx_tile<FMT, T>;
+  auto kern = fused ? k_mx_tile<FMT, T, true> : k_mx_tile<FMT, T, false>;
   CK(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
   cudaLaunchConfig_t lc = {};
   lc.gridDim = dim3((unsigned)(tiles * ranks));
@@ -261,6 +277,34 @@ bool dtype_ok(int dtype) { return dtype >= ADMMQ_DTYPE_F32 && dtype <= ADMMQ_DTY
 
 namespace {
 
+MxArgs mx_args(const uint8_t* a_scale, const float* a_tensor_scale, const uint8_t* b_scale,
+               const float* b_tensor_scale, int64_t m, int n, int k, int fmt, void* out) {
+  MxArgs p;
+  p.w_scale = b_scale;
+  p.x_scale = a_scale;
+  p.gw = b_tensor_scale;
+  p.gx = a_tensor_scale;
+  p.out = out;
+  p.m = (int)m;
+  p.n = n;
+  p.k = k;
+  p.tn = m <= 128 ? ((int)m + 15) / 16 * 16 : 256;
+  p.tiles_n = cdiv(n, 128);
+  p.kblocks = cdiv(k, kMxBK);
+  p.col_tiles = cdiv(k, mx_tile_k(fmt));
+  p.raw = nullptr;
+  return p;
+}
+
+// Whether admmq_mx_linear quantises inside the product.
+bool mx_linear_fused(int64_t m, int n, int k, int fmt) {
+  if (m > kFusedTokens) return false;
+  MxArgs p = mx_args(nullptr, nullptr, nullptr, nullptr, m, n, k, fmt, nullptr);
+  bool fits;
+  plan_tile(p, fmt, fits);
+  return fits;
+}
+
 // The product of two MX matrices; check_only: its argument checks alone.
 int mx_product(const uint8_t* a_codes, const uint8_t* a_scale, const float* a_tensor_scale,
                     const uint8_t* b_codes, const uint8_t* b_scale, const float* b_tensor_scale,
@@ -276,25 +320,13 @@ int mx_product(const uint8_t* a_codes, const uint8_t* a_scale, const float* a_te
     return ADMMQ_ERR_INVALID_ARG;
   int rc = device_ok();
   if (rc || check_only) return rc;
-  MxArgs p;
-  p.w_scale = b_scale;
-  p.x_scale = a_scale;
-  p.gw = b_tensor_scale;
-  p.gx = a_tensor_scale;
-  p.out = out;
-  p.m = (int)m;
-  p.n = n;
-  p.k = k;
-  p.tn = m <= 128 ? ((int)m + 15) / 16 * 16 : 256;
-  p.tiles_n = cdiv(n, 128);
-  p.kblocks = cdiv(k, kMxBK);
-  p.col_tiles = cdiv(k, mx_tile_k(fmt));
+  MxArgs p = mx_args(a_scale, a_tensor_scale, b_scale, b_tensor_scale, m, n, k, fmt, out);
   const bool pair = m > 128;
   if (!pair && (!make_codes_map(&p.w, b_codes, k, n, 128) || !make_codes_map(&p.x, a_codes, k, m, p.tn)))
     return ADMMQ_ERR_CUDA;
 #define PRODUCT(FMT, T)                                                            \
   rc = pair ? launch_pair<FMT, T>(b_codes, a_codes, p, (cudaStream_t)stream)       \
-            : launch_tile<FMT, T>(p, (cudaStream_t)stream)
+            : launch_tile<FMT, T>(p, false, (cudaStream_t)stream)
   MX_DISPATCH(fmt, out_dtype, PRODUCT)
 #undef PRODUCT
   return rc;
@@ -364,8 +396,10 @@ int admmq_mx_matmul(const uint8_t* a_codes, const uint8_t* a_scale, const float*
                     out, out_dtype, stream, false);
 }
 
-size_t admmq_mx_linear_workspace_bytes(int64_t m, int k, int fmt) {
-  if (!mx_shape_ok(m, k, fmt)) return 0;
+size_t admmq_mx_linear_workspace_bytes(int64_t m, int n, int k, int fmt) {
+  if (!mx_shape_ok(m, k, fmt) || !mx_shape_ok(n, k, fmt) || n < 1 || m == 0 ||
+      mx_linear_fused(m, n, k, fmt))
+    return 0;
   return (((size_t)m * (k / 2) + 255) & ~(size_t)255) + admmq_mx_scale_bytes(m, k, fmt);
 }
 
@@ -376,14 +410,28 @@ int admmq_mx_linear(const void* x, int x_dtype, int64_t m, int64_t ldx, const fl
   if (!mx_shape_ok(m, k, fmt) || !dtype_ok(x_dtype) || !dtype_ok(out_dtype) || n < 1 || ldx < k)
     return ADMMQ_ERR_INVALID_ARG;
   if (m == 0) return ADMMQ_OK;
-  if (!x || !w_codes || !w_scale || !out || !ws || ((uintptr_t)ws & 255)) return ADMMQ_ERR_INVALID_ARG;
-  if (ws_bytes < admmq_mx_linear_workspace_bytes(m, k, fmt)) return ADMMQ_ERR_WORKSPACE;
-  uint8_t* codes = (uint8_t*)ws;
-  uint8_t* scale = codes + (((size_t)m * (k / 2) + 255) & ~(size_t)255);
+  if (!x || !aligned16(x) || ldx * dtype_size(x_dtype) % 16 != 0) return ADMMQ_ERR_INVALID_ARG;
+  const bool fused = mx_linear_fused(m, n, k, fmt);
+  if (!fused && (!ws || ((uintptr_t)ws & 255))) return ADMMQ_ERR_INVALID_ARG;
+  if (ws_bytes < admmq_mx_linear_workspace_bytes(m, n, k, fmt)) return ADMMQ_ERR_WORKSPACE;
+  uint8_t* codes = fused ? (uint8_t*)w_codes : (uint8_t*)ws;  // (fused: checked, not used)
+  uint8_t* scale = fused ? (uint8_t*)w_scale : codes + (((size_t)m * (k / 2) + 255) & ~(size_t)255);
   // the product's arguments first: nothing is launched when they are refused
   int rc = mx_product(codes, scale, x_tensor_scale, w_codes, w_scale, w_tensor_scale, m, n, k, fmt,
                       out, out_dtype, stream, true);
   if (rc) return rc;
+  if (fused) {
+    MxArgs p = mx_args(nullptr, x_tensor_scale, w_scale, w_tensor_scale, m, n, k, fmt, out);
+    p.raw = x;
+    p.ld = ldx;
+    p.raw_dtype = x_dtype;
+    if (!make_codes_map(&p.w, w_codes, k, n, 128)) return ADMMQ_ERR_CUDA;
+    p.x = p.w;  // not used
+#define FUSED(FMT, T) rc = launch_tile<FMT, T>(p, true, (cudaStream_t)stream)
+    MX_DISPATCH(fmt, out_dtype, FUSED)
+#undef FUSED
+    return rc;
+  }
   rc = admmq_mx_quantize(x, x_dtype, m, k, ldx, fmt, x_tensor_scale, codes, scale, stream);
   if (rc) return rc;
   return mx_product(codes, scale, x_tensor_scale, w_codes, w_scale, w_tensor_scale, m, n, k, fmt,

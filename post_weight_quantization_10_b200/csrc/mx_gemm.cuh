@@ -7,6 +7,7 @@
 // of one token, which out stores next to each other.
 #pragma once
 #include "async.cuh"
+#include "../../include/admmq.h"
 #include "mx.cuh"
 #include "ptx.cuh"
 
@@ -74,18 +75,49 @@ struct MxArgs {
   int tiles_n;                 // 128-column tiles
   int kblocks, col_tiles;      // 256-element stages; scale tiles along k
   int stages, stage_bytes, part_bytes;  // part_bytes: the ranks' partial tiles
+  const void* raw;             // k_mx_tile<..., true>: the activations themselves,
+  long long ld;                // their row distance
+  int raw_dtype;               // and type
   int tmem_cols;
 };
 
 constexpr int kMxBK = 256;  // elements of K per stage: 128-byte rows
 constexpr int kMxTileThreads = 192;
 
+// One warp quantises 256 columns from `col` of one row: as k_mx_quantize does,
+// into a stage's swizzled code rows and its scale tiles.  What lies behind the
+// last column is zero (codes and scales).
+template <int FMT, typename X>
+__device__ __forceinline__ void quantize_into(const X* x, int k, int col, int row, float g, float r6g,
+                                              uint8_t* codes, uint8_t* scales) {
+  constexpr int LANES = MxFormat<FMT>::BLOCK / 16;
+  const int lane = threadIdx.x & 31;
+  if (lane >= 16) return;   // sixteen elements a lane
+  const bool in = col + 16 * lane < k;
+  Raw16<X> raw;
+#pragma unroll
+  for (int i = 0; i < (int)(4 * sizeof(X)); ++i) raw.w[i] = 0u;
+  if (in) load_raw(x + col + 16 * lane, false, raw);
+  float v[16];
+  values_of(raw, v);
+  uint32_t amax = amax_of(raw);
+  if (LANES == 2) amax = max(amax, __shfl_xor_sync(0xFFFFu, amax, 1));
+  const uint32_t byte = in ? block_scale<FMT>(amax, g, r6g) : 0u;
+  const uint2 out = quantize16<FMT>(v, byte, g);
+  *reinterpret_cast<uint2*>(codes + row * 128 + (((lane >> 1) ^ (row & 7)) << 4) + 8 * (lane & 1)) = out;
+  const int c = lane / LANES;
+  if (lane % LANES == 0) scales[(c >> 2) * kScaleTile + scale_at(row, c & 3)] = (uint8_t)byte;
+}
+
 // One output tile of 128 columns x tn tokens per cluster; the cluster's CTAs
 // share the reduction (contiguous ranges of stages); each rank sums a share of
 // the tokens, from partial tiles that all ranks store into its shared memory,
 // in rank order.
+// FUSED (a few tokens, every stage of a block resident): the activations are
+// quantised here, by the epilogue's warps while the weights are on their way,
+// instead of by a launch of their own.
 //   warp 0  TMA producer    warp 1  MMA issuer    warps 2-5  epilogue
-template <int FMT, typename T>
+template <int FMT, typename T, bool FUSED>
 __global__ void __launch_bounds__(kMxTileThreads)
     k_mx_tile(const __grid_constant__ MxArgs p) {
   constexpr int NSF = kMxBK / MxFormat<FMT>::TILE_K;  // scale tiles per stage and 128 rows
@@ -99,7 +131,8 @@ __global__ void __launch_bounds__(kMxTileThreads)
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + p.stages * p.stage_bytes + p.part_bytes);
   uint64_t* empty = full + p.stages;
   uint64_t* done = empty + p.stages;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
+  uint64_t* quantised = done + 1;  // FUSED: the activations' codes and scales are there
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(quantised + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -117,6 +150,7 @@ __global__ void __launch_bounds__(kMxTileThreads)
       mbar_init(smem_u32(&empty[s]), 1);
     }
     mbar_init(smem_u32(done), 1);
+    mbar_init(smem_u32(quantised), 4);
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -143,11 +177,11 @@ __global__ void __launch_bounds__(kMxTileThreads)
         }
         const uint32_t bar = smem_u32(&full[r.i]), st = smem_u32(smem + r.i * p.stage_bytes);
         const int sf = min(NSF, p.col_tiles - kb * NSF) * kScaleTile;  // scale bytes of this stage
-        mbar_arrive_expect_tx(bar, 128 * 128 + x_bytes + sf * (1 + xrows));
+        mbar_arrive_expect_tx(bar, 128 * 128 + sf + (FUSED ? 0 : x_bytes + sf * xrows));
         tma_load_2d(st, &p.w, kb * 128, tn_tile * 128, bar);
-        tma_load_2d(st + x_off, &p.x, kb * 128, tm_tile * p.tn, bar);
         bulk_load(st + sw_off, ws, sf, bar);
-        for (int i = 0; i < xrows; ++i)
+        if (!FUSED) tma_load_2d(st + x_off, &p.x, kb * 128, tm_tile * p.tn, bar);
+        for (int i = 0; i < (FUSED ? 0 : xrows); ++i)
           bulk_load(st + sx_off + i * NSF * kScaleTile, xs + (long long)i * p.col_tiles * kScaleTile,
                     sf, bar);
         ws += NSF * kScaleTile;
@@ -164,8 +198,9 @@ __global__ void __launch_bounds__(kMxTileThreads)
     const uint64_t dx0 = smem_desc_sw128(smem_u32(smem) + x_off, 16, 1024);
     const uint64_t dsw0 = scale_desc(smem_u32(smem) + sw_off), dsx0 = scale_desc(smem_u32(smem) + sx_off);
     Ring r;
+    const bool there = !FUSED || mbar_wait(smem_u32(quantised), 0, abort_flag, nullptr);
     for (int kb = kb0; kb < kb1; ++kb) {
-      const bool ok = mbar_wait(smem_u32(&full[r.i]), r.phase, abort_flag, nullptr);
+      const bool ok = there && mbar_wait(smem_u32(&full[r.i]), r.phase, abort_flag, nullptr);
       if (!__all_sync(~0u, ok)) break;
       tc_fence_after();
       const uint32_t at = r.i * (p.stage_bytes >> 4);
@@ -208,6 +243,25 @@ __global__ void __launch_bounds__(kMxTileThreads)
   T* out = reinterpret_cast<T*>(p.out) + (long long)tm_tile * p.tn * p.n + col;
   const int per = (tokens + (int)ranks - 1) / (int)ranks;  // tokens that a rank sums
   const uint32_t part = smem_u32(smem) + p.stages * p.stage_bytes;  // [ranks][per][128]
+  if (FUSED && warp >= 2) {
+    const float gx = p.gx ? *p.gx : 1.f, r6g = 1.f / (6.f * gx);
+    const int items = p.m * (kb1 - kb0);
+    for (int i = warp - 2; i < items; i += 4) {
+      const int s = i / p.m, token = i - s * p.m, c = (kb0 + s) * kMxBK;
+      uint8_t* st = smem + s * p.stage_bytes;
+      const long long at = token * p.ld;
+      if (p.raw_dtype == ADMMQ_DTYPE_BF16)
+        quantize_into<FMT>((const __nv_bfloat16*)p.raw + at, p.k, c, token, gx, r6g, st + x_off, st + sx_off);
+      else if (p.raw_dtype == ADMMQ_DTYPE_F16)
+        quantize_into<FMT>((const __half*)p.raw + at, p.k, c, token, gx, r6g, st + x_off, st + sx_off);
+      else
+        quantize_into<FMT>((const float*)p.raw + at, p.k, c, token, gx, r6g, st + x_off, st + sx_off);
+      __syncwarp();
+    }
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(quantised));
+  }
   if (warp >= 2) {
     ok = mbar_wait(smem_u32(done), 0, abort_flag, nullptr);
     ok = __all_sync(~0u, ok) && !*abort_flag;

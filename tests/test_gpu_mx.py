@@ -215,7 +215,7 @@ def test_product_writes_its_rows_only(A):
 
 def test_linear_is_quantize_then_product(A):
     for fmt in mx.BLOCK:
-        for m in (1, 9, 40, 200):
+        for m in (1, 3, 9, 16, 17, 40, 200):
             x = _matrix(m, 320, m, torch.bfloat16).cuda()
             w = _matrix(210, 320, 3).cuda()
             g = _dev_g(_g(x)) if fmt == "nvfp4" else None

@@ -84,3 +84,20 @@ def test_binding_refuses_host_tensors():
         with pytest.raises(A.AdmmqError) as e:
             call()
         assert e.value.status == INVALID
+
+
+def test_linear_refusals(lib):
+    # x dtype m ldx gx, w: codes scale g, n k fmt out dtype ws ws_bytes stream
+    good = [_p(0), 1, 40, 64, _p(1), _p(2), _p(3), _p(4), 16, 64, 1, _p(5), 1, _p(6), 1 << 30, None]
+    off = ctypes.c_void_p(0x10008)
+    _refused(lib.admmq_mx_linear, good,
+             [(0, None), (0, off), (1, 3), (2, -1), (3, 32), (3, 68), (4, ctypes.c_void_p(2)),
+              (5, None), (5, off), (6, None), (6, off), (7, ctypes.c_void_p(2)), (8, 0), (9, 40),
+              (10, 2), (10, 0), (11, None), (11, off), (12, 5), (13, None),
+              (13, ctypes.c_void_p(0x10080))])
+    bad = list(good)
+    bad[14] = 100
+    assert lib.admmq_mx_linear(*bad) == -7
+    f = lib.admmq_mx_linear_workspace_bytes
+    assert f(0, 16, 64, 0) == 0 and f(40, 16, 48, 0) == 0 and f(40, 0, 64, 0) == 0
+    assert f(40, 16, 64, 0) == (40 * 32 + 255) // 256 * 256 + 512
