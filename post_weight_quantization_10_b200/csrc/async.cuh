@@ -49,6 +49,17 @@ __device__ __forceinline__ void st_cluster_f32(uint32_t addr_cluster, float v) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr_cluster), "f"(v) : "memory");
 }
 
+// A kernel that another one is launched to overlap with (programmatic
+// dependent launch): from here on the other may start; and in the other: what
+// comes after this sees everything the first kernel wrote.  Without that launch
+// attribute both do nothing.
+__device__ __forceinline__ void let_next_kernel_start() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void wait_for_previous_kernel() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 // True for one lane of the (converged) warp.  A role that issues tcgen05
 // instructions runs on its whole warp and elects a lane for the issue alone:
 // descriptors and loop state then stay in uniform registers.

@@ -1,6 +1,7 @@
 // mx.cu -- microscaled 4-bit floating point matrices (mxfp4, nvfp4):
 // quantisation, dequantisation and the product of two of them.
 #include "host.cuh"
+#include "async.cuh"
 #include "mx.cuh"
 #include "mx_gemm.cuh"
 #include "tmem_fair.cuh"
@@ -15,7 +16,7 @@ namespace {
 // block, or half of an mxfp4 one, whose two lanes share its largest magnitude.
 constexpr int kSpan = 512;  // columns of a thread block
 constexpr int kMxThreads = 256;
-constexpr int kMxRows = 128 / (kMxThreads / 32);  // rows of a warp
+constexpr int kMxWarps = kMxThreads / 32;  // warp w takes rows w, w + 8, ...
 
 template <int FMT, typename T>
 __global__ void __launch_bounds__(kMxThreads)
@@ -26,6 +27,7 @@ __global__ void __launch_bounds__(kMxThreads)
   constexpr int LANES = MxFormat<FMT>::BLOCK / 16;  // lanes that share a block
   constexpr int TILES = kSpan / TILE_K;
   __shared__ __align__(16) uint8_t tile[TILES * kScaleTile];
+  let_next_kernel_start();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const long long row_tile = blockIdx.x / spans;
   const int span = (int)(blockIdx.x - row_tile * spans);
@@ -40,11 +42,12 @@ __global__ void __launch_bounds__(kMxThreads)
     for (int i = threadIdx.x; i < TILES * kScaleTile / 16; i += kMxThreads)
       reinterpret_cast<uint4*>(tile)[i] = make_uint4(0, 0, 0, 0);
   __syncthreads();
-  const T* src = x + (row_tile * 128 + warp * kMxRows) * ld + col;
-  uint8_t* dst = codes + ((row_tile * 128 + warp * kMxRows) * k + col) / 2;
+  const T* src = x + (row_tile * 128 + warp) * ld + col;
+  uint8_t* dst = codes + ((row_tile * 128 + warp) * k + col) / 2;
+  const long long src_step = ld * kMxWarps, dst_step = (long long)(k / 2) * kMxWarps;
   const int c = lane / LANES;
   uint8_t* to = tile + (c >> 2) * kScaleTile + (c & 3);
-  const int n = min(kMxRows, last - warp * kMxRows);
+  const int n = (last - warp + kMxWarps - 1) / kMxWarps;
   // a block's lanes are inside or outside together; all stay for the shuffle
   const bool in = col < k;
   const bool wide = (((uintptr_t)x | (uintptr_t)(ld * sizeof(T))) & 31) == 0;
@@ -57,9 +60,9 @@ __global__ void __launch_bounds__(kMxThreads)
     for (int j = 0; j < AHEAD; ++j) {
 #pragma unroll
       for (int i = 0; i < (int)(4 * sizeof(T)); ++i) raw[j].w[i] = 0u;
-      if (in && j0 + j < n) load_raw(src + j * ld, wide, raw[j]);
+      if (in && j0 + j < n) load_raw(src + j * src_step, wide, raw[j]);
     }
-    src += AHEAD * ld;
+    src += AHEAD * src_step;
 #pragma unroll
     for (int j = 0; j < AHEAD; ++j) {
       if (j0 + j >= n) break;
@@ -71,9 +74,9 @@ __global__ void __launch_bounds__(kMxThreads)
       const uint2 out = quantize16<FMT>(v, byte, g);
       if (in) {
         *reinterpret_cast<uint2*>(dst) = out;
-        if (lane % LANES == 0) to[scale_at(warp * kMxRows + j0 + j, 0)] = (uint8_t)byte;
+        if (lane % LANES == 0) to[scale_at((j0 + j) * kMxWarps + warp, 0)] = (uint8_t)byte;
       }
-      dst += k / 2;
+      dst += dst_step;
     }
   }
   __syncthreads();
@@ -105,9 +108,10 @@ __global__ void __launch_bounds__(kMxThreads)
   __syncthreads();
   if (col >= k) return;
   const int last = rows - row_tile * 128 < 128 ? (int)(rows - row_tile * 128) : 128;
-  const int n = min(kMxRows, last - warp * kMxRows);
-  const uint8_t* src = codes + ((row_tile * 128 + warp * kMxRows) * k + col) / 2;
-  T* dst = out + (row_tile * 128 + warp * kMxRows) * ld + col;
+  const int n = (last - warp + kMxWarps - 1) / kMxWarps;
+  const uint8_t* src = codes + ((row_tile * 128 + warp) * k + col) / 2;
+  T* dst = out + (row_tile * 128 + warp) * ld + col;
+  const long long src_step = (long long)(k / 2) * kMxWarps, dst_step = ld * kMxWarps;
   const int c = lane / LANES;
   const uint8_t* from = tile + (c >> 2) * kScaleTile + (c & 3);
   const bool wide = (((uintptr_t)out | (uintptr_t)(ld * sizeof(T))) & 31) == 0;
@@ -116,12 +120,12 @@ __global__ void __launch_bounds__(kMxThreads)
     uint2 w[AHEAD];
 #pragma unroll
     for (int j = 0; j < AHEAD; ++j)
-      w[j] = j0 + j < n ? __ldg(reinterpret_cast<const uint2*>(src + (long long)j * (k / 2))) : make_uint2(0, 0);
-    src += (long long)AHEAD * (k / 2);
+      w[j] = j0 + j < n ? __ldg(reinterpret_cast<const uint2*>(src + j * src_step)) : make_uint2(0, 0);
+    src += AHEAD * src_step;
 #pragma unroll
     for (int j = 0; j < AHEAD; ++j) {
       if (j0 + j >= n) break;
-      const float t = block_step<FMT>(from[scale_at(warp * kMxRows + j0 + j, 0)], g);
+      const float t = block_step<FMT>(from[scale_at((j0 + j) * kMxWarps + warp, 0)], g);
       float v[16];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
@@ -132,7 +136,7 @@ __global__ void __launch_bounds__(kMxThreads)
       Raw16<T> r;
       raw_of(v, r);
       store_raw(dst, wide, r);
-      dst += ld;
+      dst += dst_step;
     }
   }
 }
@@ -198,8 +202,17 @@ int launch_pair(const uint8_t* w_codes, const uint8_t* x_codes, const MxArgs& q,
   CK(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
   const int pairs = num_sms() / 2;
   count_launch();
-  kern<<<2 * (p.tiles < pairs ? p.tiles : pairs), kMxPairThreads, smem, st>>>(p);
-  CK(cudaGetLastError());
+  cudaLaunchConfig_t lc = {};
+  lc.gridDim = dim3((unsigned)(2 * (p.tiles < pairs ? p.tiles : pairs)));
+  lc.blockDim = dim3(kMxPairThreads);
+  lc.dynamicSmemBytes = smem;
+  lc.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  lc.attrs = attr;
+  lc.numAttrs = q.overlap ? 1 : 0;
+  CK(cudaLaunchKernelEx(&lc, kern, p));
   return ADMMQ_OK;
 }
 
@@ -243,13 +256,15 @@ int launch_tile(MxArgs& p, bool fused, cudaStream_t st) {
   lc.blockDim = dim3(kMxTileThreads);
   lc.dynamicSmemBytes = smem;
   lc.stream = st;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = ranks;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   lc.attrs = attr;
-  lc.numAttrs = 1;
+  lc.numAttrs = p.overlap ? 2 : 1;
   count_launch();
   CK(cudaLaunchKernelEx(&lc, kern, p));
   return ADMMQ_OK;
@@ -293,6 +308,7 @@ MxArgs mx_args(const uint8_t* a_scale, const float* a_tensor_scale, const uint8_
   p.kblocks = cdiv(k, kMxBK);
   p.col_tiles = cdiv(k, mx_tile_k(fmt));
   p.raw = nullptr;
+  p.overlap = 0;
   return p;
 }
 
@@ -308,7 +324,7 @@ bool mx_linear_fused(int64_t m, int n, int k, int fmt) {
 // The product of two MX matrices; check_only: its argument checks alone.
 int mx_product(const uint8_t* a_codes, const uint8_t* a_scale, const float* a_tensor_scale,
                     const uint8_t* b_codes, const uint8_t* b_scale, const float* b_tensor_scale,
-                    int64_t m, int n, int k, int fmt, void* out, int out_dtype, void* stream, bool check_only) {
+                    int64_t m, int n, int k, int fmt, void* out, int out_dtype, void* stream, bool check_only, bool overlap) {
   if (!mx_shape_ok(m, k, fmt) || !mx_shape_ok(n, k, fmt) || n < 1 || !dtype_ok(out_dtype))
     return ADMMQ_ERR_INVALID_ARG;
   if (fmt == ADMMQ_MX_MXFP4 && (a_tensor_scale || b_tensor_scale)) return ADMMQ_ERR_INVALID_ARG;
@@ -321,6 +337,7 @@ int mx_product(const uint8_t* a_codes, const uint8_t* a_scale, const float* a_te
   int rc = device_ok();
   if (rc || check_only) return rc;
   MxArgs p = mx_args(a_scale, a_tensor_scale, b_scale, b_tensor_scale, m, n, k, fmt, out);
+  p.overlap = overlap;
   const bool pair = m > 128;
   if (!pair && (!make_codes_map(&p.w, b_codes, k, n, 128) || !make_codes_map(&p.x, a_codes, k, m, p.tn)))
     return ADMMQ_ERR_CUDA;
@@ -393,7 +410,7 @@ int admmq_mx_matmul(const uint8_t* a_codes, const uint8_t* a_scale, const float*
                     const uint8_t* b_codes, const uint8_t* b_scale, const float* b_tensor_scale,
                     int64_t m, int n, int k, int fmt, void* out, int out_dtype, void* stream) {
   return mx_product(a_codes, a_scale, a_tensor_scale, b_codes, b_scale, b_tensor_scale, m, n, k, fmt,
-                    out, out_dtype, stream, false);
+                    out, out_dtype, stream, false, false);
 }
 
 size_t admmq_mx_linear_workspace_bytes(int64_t m, int n, int k, int fmt) {
@@ -418,7 +435,7 @@ int admmq_mx_linear(const void* x, int x_dtype, int64_t m, int64_t ldx, const fl
   uint8_t* scale = fused ? (uint8_t*)w_scale : codes + (((size_t)m * (k / 2) + 255) & ~(size_t)255);
   // the product's arguments first: nothing is launched when they are refused
   int rc = mx_product(codes, scale, x_tensor_scale, w_codes, w_scale, w_tensor_scale, m, n, k, fmt,
-                      out, out_dtype, stream, true);
+                      out, out_dtype, stream, true, false);
   if (rc) return rc;
   if (fused) {
     MxArgs p = mx_args(nullptr, x_tensor_scale, w_scale, w_tensor_scale, m, n, k, fmt, out);
@@ -434,8 +451,11 @@ int admmq_mx_linear(const void* x, int x_dtype, int64_t m, int64_t ldx, const fl
   }
   rc = admmq_mx_quantize(x, x_dtype, m, k, ldx, fmt, x_tensor_scale, codes, scale, stream);
   if (rc) return rc;
+  // The product starts while the quantisation in front of it runs (an ordinary
+  // launch, so everything before it is done): it reads the weights at once and
+  // the activations when they are there.
   return mx_product(codes, scale, x_tensor_scale, w_codes, w_scale, w_tensor_scale, m, n, k, fmt,
-                    out, out_dtype, stream, false);
+                    out, out_dtype, stream, false, true);
 }
 
 }  // extern "C"

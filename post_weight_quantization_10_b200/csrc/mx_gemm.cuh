@@ -78,6 +78,7 @@ struct MxArgs {
   const void* raw;             // k_mx_tile<..., true>: the activations themselves,
   long long ld;                // their row distance
   int raw_dtype;               // and type
+  int overlap;                 // launched to overlap with the kernel in front
   int tmem_cols;
 };
 
@@ -167,25 +168,41 @@ __global__ void __launch_bounds__(kMxTileThreads)
       Ring r;
       int loads = 0;
       // a token tile's 128-row scale tiles that exist
-      const int x_row = tm_tile * p.tn >> 7, xrows = min(xt, (p.m + 127) / 128 - x_row);
-      const uint8_t* ws = p.w_scale + ((long long)tn_tile * p.col_tiles + kb0 * NSF) * kScaleTile;
-      const uint8_t* xs = p.x_scale + ((long long)x_row * p.col_tiles + kb0 * NSF) * kScaleTile;
-      for (int kb = kb0; kb < kb1; ++kb, ++loads) {
+      const int x_row = tm_tile * p.tn >> 7, xrows = FUSED ? 0 : min(xt, (p.m + 127) / 128 - x_row);
+      const uint8_t* ws = p.w_scale + (long long)tn_tile * p.col_tiles * kScaleTile;
+      const uint8_t* xs = p.x_scale + (long long)x_row * p.col_tiles * kScaleTile;
+      auto load_w = [&](int kb, uint32_t st, uint32_t bar) {
+        const int sf = min(NSF, p.col_tiles - kb * NSF) * kScaleTile;  // scale bytes of this stage
+        mbar_arrive_expect_tx(bar, 128 * 128 + sf + (FUSED ? 0 : x_bytes + sf * xrows));
+        tma_load_2d(st, &p.w, kb * 128, tn_tile * 128, bar);
+        bulk_load(st + sw_off, ws + kb * NSF * kScaleTile, sf, bar);
+      };
+      auto load_x = [&](int kb, uint32_t st, uint32_t bar) {
+        const int sf = min(NSF, p.col_tiles - kb * NSF) * kScaleTile;
+        tma_load_2d(st + x_off, &p.x, kb * 128, tm_tile * p.tn, bar);
+        for (int i = 0; i < xrows; ++i)
+          bulk_load(st + sx_off + i * NSF * kScaleTile,
+                    xs + ((long long)i * p.col_tiles + kb * NSF) * kScaleTile, sf, bar);
+      };
+      // the weights of every stage before the first activation, which the
+      // kernel in front may still be writing
+      const int first = min(p.stages, kb1 - kb0);
+      const uint32_t st0 = smem_u32(smem), bar0 = smem_u32(full);
+      for (int s = 0; s < first; ++s) load_w(kb0 + s, st0 + s * p.stage_bytes, bar0 + 8 * s);
+      if (!FUSED) {
+        wait_for_previous_kernel();
+        for (int s = 0; s < first; ++s) load_x(kb0 + s, st0 + s * p.stage_bytes, bar0 + 8 * s);
+      }
+      loads = first;
+      r.phase = 1;  // the ring's second round
+      for (int kb = kb0 + first; kb < kb1; ++kb, ++loads) {
         if (!mbar_wait(smem_u32(&empty[r.i]), r.phase ^ 1u, abort_flag, nullptr)) {
           ok = false;
           break;
         }
-        const uint32_t bar = smem_u32(&full[r.i]), st = smem_u32(smem + r.i * p.stage_bytes);
-        const int sf = min(NSF, p.col_tiles - kb * NSF) * kScaleTile;  // scale bytes of this stage
-        mbar_arrive_expect_tx(bar, 128 * 128 + sf + (FUSED ? 0 : x_bytes + sf * xrows));
-        tma_load_2d(st, &p.w, kb * 128, tn_tile * 128, bar);
-        bulk_load(st + sw_off, ws, sf, bar);
-        if (!FUSED) tma_load_2d(st + x_off, &p.x, kb * 128, tm_tile * p.tn, bar);
-        for (int i = 0; i < (FUSED ? 0 : xrows); ++i)
-          bulk_load(st + sx_off + i * NSF * kScaleTile, xs + (long long)i * p.col_tiles * kScaleTile,
-                    sf, bar);
-        ws += NSF * kScaleTile;
-        xs += NSF * kScaleTile;
+        const uint32_t bar = bar0 + 8 * r.i, st = st0 + r.i * p.stage_bytes;
+        load_w(kb, st, bar);
+        if (!FUSED) load_x(kb, st, bar);
         r.next(p.stages);
       }
       if (!ok)
@@ -407,6 +424,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxPairThreads, 1)
       Ring r;
       int loads = 0;
       const uint32_t full0 = cluster_addr(full, 0);
+      wait_for_previous_kernel();
       for (int tile = pair0; tile < p.tiles && ok; tile += pairs) {
         const int tn = tile / p.tiles_m, tm = tile - tn * p.tiles_m;
         const int w_row = tn * 256 + (int)rank * 128, x_row = tm * 256 + (int)rank * 128;
