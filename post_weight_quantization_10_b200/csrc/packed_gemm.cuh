@@ -113,14 +113,13 @@ __device__ __forceinline__ void decode_chunk(const PackedGemmArgs& a, const uint
 
 // Shared-memory addresses of the barriers (arrays of 8-byte words).
 struct PackedBars {
-  uint32_t full_x, full_a, empty;  // [stages]: activations, decoded weights; stage read
+  uint32_t full, empty;            // [stages]: activations and decoded weights there; read
   uint32_t wfull, wempty;          // [wbufs]: packed chunk there; decoded
   uint32_t rfull, rempty, drain;   // [2]: group finished; added; everything finished
   uint32_t end;
   __device__ PackedBars(uint32_t at, int stages, int wbufs) {
-    full_x = at;
-    full_a = full_x + 8 * stages;
-    empty = full_a + 8 * stages;
+    full = at;
+    empty = full + 8 * stages;
     wfull = empty + 8 * stages;
     wempty = wfull + 8 * wbufs;
     rfull = wempty + 8 * wbufs;
@@ -130,9 +129,9 @@ struct PackedBars {
   }
 };
 
-// The MMA warp's loop: 8 MMAs of K = 16 per chunk, PASSES groups.
+// The MMA thread's loop: 8 MMAs of K = 16 per chunk, PASSES groups.
 template <typename X, int TN, int C, int PASSES>
-__device__ __forceinline__ bool issue_mmas(const PackedGemmArgs& a, int ch0, int ch1, int tile0,
+__device__ __forceinline__ void issue_mmas(const PackedGemmArgs& a, int ch0, int ch1, int tile0,
                                            int tile_step, uint32_t tmem, const uint8_t* smem,
                                            const PackedBars& bars, volatile int* abort_flag) {
   using Cfg = PackedCfg<TN, C>;
@@ -146,8 +145,8 @@ __device__ __forceinline__ bool issue_mmas(const PackedGemmArgs& a, int ch0, int
       const int groups = min(PASSES, a.p.groups - ch * PASSES);  // of this chunk
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        bool ok = mbar_wait(bars.full_x + 8 * st.i, st.phase, abort_flag, nullptr) &&
-                  mbar_wait(bars.full_a + 8 * st.i, st.phase, abort_flag, nullptr);
+        if (!mbar_wait(bars.full + 8 * st.i, st.phase, abort_flag, nullptr)) return;
+        tc_fence_after();
         const uint64_t dx = dx0 + (uint32_t)(st.i * (Cfg::STAGE >> 4));
         const uint64_t dw = dw0 + (uint32_t)(st.i * (Cfg::STAGE >> 4));
         // the half's MMAs, a group (or the half of one) at a time
@@ -155,34 +154,28 @@ __device__ __forceinline__ bool issue_mmas(const PackedGemmArgs& a, int ch0, int
         for (int j0 = 0; j0 < 4; j0 += PER < 4 ? PER : 4) {
           const int step = 4 * h + j0;
           if (step / PER < groups) {
-            if (step % PER == 0)
-              ok = ok && mbar_wait(bars.rempty + 8 * slot.i, slot.phase ^ 1u, abort_flag, nullptr);
-            if (!__all_sync(~0u, ok)) return false;
-            tc_fence_after();
-            const bool ends = (step + (PER < 4 ? PER : 4)) % PER == 0;
-            if (elect_one()) {
-#pragma unroll
-              for (int j = j0; j < j0 + (PER < 4 ? PER : 4); ++j)
-                mma_f16(tmem + slot.i * TN, dw + 2 * j, dx + 2 * j, IDESC,
-                        (4 * h + j) % PER == 0 ? 0u : 1u);
-              if (ends) mma_commit(bars.rfull + 8 * slot.i);
+            if (step % PER == 0) {
+              if (!mbar_wait(bars.rempty + 8 * slot.i, slot.phase ^ 1u, abort_flag, nullptr)) return;
+              tc_fence_after();
             }
-            __syncwarp();
-            if (ends) slot.next(2);
+#pragma unroll
+            for (int j = j0; j < j0 + (PER < 4 ? PER : 4); ++j)
+              mma_f16(tmem + slot.i * TN, dw + 2 * j, dx + 2 * j, IDESC,
+                      (4 * h + j) % PER == 0 ? 0u : 1u);
+            if ((step + (PER < 4 ? PER : 4)) % PER == 0) {
+              mma_commit(bars.rfull + 8 * slot.i);
+              slot.next(2);
+            }
           }
         }
-        if (!__all_sync(~0u, ok)) return false;
-        if (elect_one()) {  // a stage's decoders write to every CTA that uses it
-          if (C == 1) mma_commit(bars.empty + 8 * st.i);
+        // a stage's decoders write to every CTA that uses it
+        if (C == 1) mma_commit(bars.empty + 8 * st.i);
 #pragma unroll
-          for (int c = 0; c < (C > 1 ? C : 0); ++c) mma_commit(cluster_addr(bars.empty + 8 * st.i, c));
-        }
-        __syncwarp();
+        for (int c = 0; c < (C > 1 ? C : 0); ++c) mma_commit(cluster_addr(bars.empty + 8 * st.i, c));
         st.next(a.stages);
       }
     }
   }
-  return true;
 }
 
 __device__ __forceinline__ void put(float* p, float v) { *p = v; }
@@ -218,7 +211,7 @@ __global__ void __launch_bounds__(PackedCfg<TN, C>::THREADS, 1)
   const uint32_t part = smem_u32(wring + NW * wbytes);
   const PackedBars bars(part + a.part_bytes, S, NW);
   uint32_t* tmem_slot =
-      reinterpret_cast<uint32_t*>(wring + NW * wbytes + a.part_bytes + (bars.end - bars.full_x));
+      reinterpret_cast<uint32_t*>(wring + NW * wbytes + a.part_bytes + (bars.end - bars.full));
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -232,8 +225,7 @@ __global__ void __launch_bounds__(PackedCfg<TN, C>::THREADS, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
-      mbar_init(bars.full_x + 8 * s, 1);
-      mbar_init(bars.full_a + 8 * s, 4);
+      mbar_init(bars.full + 8 * s, 5);  // the activations' producer, four decoder warps
       mbar_init(bars.empty + 8 * s, C);
     }
     for (int i = 0; i < NW; ++i) {
@@ -268,7 +260,7 @@ __global__ void __launch_bounds__(PackedCfg<TN, C>::THREADS, 1)
       for (int tile = tile0; tile < a.tiles && ok; tile += tile_step) {
         const int tn = tile / a.tiles_m, tm = (tile - tn * a.tiles_m) * C + (C > 1 ? rank : 0);
         for (int k = ch0 * 128; k < ch1 * 128; k += 64, ++loads) {
-          const uint32_t bar = bars.full_x + 8 * x.i;
+          const uint32_t bar = bars.full + 8 * x.i;
           if (!mbar_wait(bars.empty + 8 * x.i, x.phase ^ 1u, abort_flag, nullptr)) {
             ok = false;
             break;
@@ -280,7 +272,7 @@ __global__ void __launch_bounds__(PackedCfg<TN, C>::THREADS, 1)
       }
       if (!ok)  // the copies in flight land before the block retires
         for (int j = max(0, loads - S); j < loads; ++j)
-          mbar_wait_drain(bars.full_x + 8 * (j % S), (uint32_t)(j / S) & 1u);
+          mbar_wait_drain(bars.full + 8 * (j % S), (uint32_t)(j / S) & 1u);
     } else if (warp == 2 && lane == 0 && a.w_tma) {
       // ----------------------------------------------- packed codes' producer
       bool ok = true;
@@ -303,11 +295,15 @@ __global__ void __launch_bounds__(PackedCfg<TN, C>::THREADS, 1)
           mbar_wait_drain(bars.wfull + 8 * (j % NW), (uint32_t)(j / NW) & 1u);
     } else if (warp == 1) {
       // -------------------------------------------------------- MMA issuer
-      const bool ok = a.passes == 1   ? issue_mmas<X, TN, C, 1>(a, ch0, ch1, tile0, tile_step, tmem, smem, bars, abort_flag)
-                      : a.passes == 2 ? issue_mmas<X, TN, C, 2>(a, ch0, ch1, tile0, tile_step, tmem, smem, bars, abort_flag)
-                                      : issue_mmas<X, TN, C, 4>(a, ch0, ch1, tile0, tile_step, tmem, smem, bars, abort_flag);
-      (void)ok;
-      if (elect_one()) mma_commit(bars.drain);
+      if (elect_one()) {
+        if (a.passes == 1)
+          issue_mmas<X, TN, C, 1>(a, ch0, ch1, tile0, tile_step, tmem, smem, bars, abort_flag);
+        else if (a.passes == 2)
+          issue_mmas<X, TN, C, 2>(a, ch0, ch1, tile0, tile_step, tmem, smem, bars, abort_flag);
+        else
+          issue_mmas<X, TN, C, 4>(a, ch0, ch1, tile0, tile_step, tmem, smem, bars, abort_flag);
+        mma_commit(bars.drain);
+      }
       __syncwarp();
       mbar_wait_drain(bars.drain, 0);
     }
@@ -394,7 +390,7 @@ __global__ void __launch_bounds__(PackedCfg<TN, C>::THREADS, 1)
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         if (lane < 2) {  // a lane for each of the two stages
-          const uint32_t i = lane ? st1.i : st0.i, bar = bars.full_a + 8 * i;
+          const uint32_t i = lane ? st1.i : st0.i, bar = bars.full + 8 * i;
           if (C == 1) {
             mbar_arrive(bar);
           } else {
