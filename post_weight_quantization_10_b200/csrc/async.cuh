@@ -60,9 +60,7 @@ __device__ __forceinline__ void wait_for_previous_kernel() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
-// True for one lane of the (converged) warp.  A role that issues tcgen05
-// instructions runs on its whole warp and elects a lane for the issue alone:
-// descriptors and loop state then stay in uniform registers.
+// True for one lane of the (converged) warp.
 __device__ __forceinline__ bool elect_one() {
   uint32_t r;
   asm volatile(

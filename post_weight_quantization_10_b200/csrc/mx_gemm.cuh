@@ -214,16 +214,16 @@ __global__ void __launch_bounds__(kMxTileThreads)
     const uint64_t dw0 = smem_desc_sw128(smem_u32(smem), 16, 1024);
     const uint64_t dx0 = smem_desc_sw128(smem_u32(smem) + x_off, 16, 1024);
     const uint64_t dsw0 = scale_desc(smem_u32(smem) + sw_off), dsx0 = scale_desc(smem_u32(smem) + sx_off);
-    Ring r;
-    const bool there = !FUSED || mbar_wait(smem_u32(quantised), 0, abort_flag, nullptr);
-    for (int kb = kb0; kb < kb1; ++kb) {
-      const bool ok = there && mbar_wait(smem_u32(&full[r.i]), r.phase, abort_flag, nullptr);
-      if (!__all_sync(~0u, ok)) break;
-      tc_fence_after();
-      const uint32_t at = r.i * (p.stage_bytes >> 4);
-      const int steps = min(4, (p.k - kb * kMxBK + 63) >> 6);
-      const int tiles = min(NSF, p.col_tiles - kb * NSF);
-      if (elect_one()) {
+    if (elect_one()) {
+      Ring r;
+      bool ok = !FUSED || mbar_wait(smem_u32(quantised), 0, abort_flag, nullptr);
+      for (int kb = kb0; kb < kb1 && ok; ++kb) {
+        ok = mbar_wait(smem_u32(&full[r.i]), r.phase, abort_flag, nullptr);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t at = r.i * (p.stage_bytes >> 4);
+        const int steps = min(4, (p.k - kb * kMxBK + 63) >> 6);
+        const int tiles = min(NSF, p.col_tiles - kb * NSF);
 #pragma unroll
         for (int i = 0; i < NSF; ++i) {
           if (i < tiles) {
@@ -243,11 +243,10 @@ __global__ void __launch_bounds__(kMxTileThreads)
           }
         }
         mma_commit(smem_u32(&empty[r.i]));
+        r.next(p.stages);
       }
-      __syncwarp();
-      r.next(p.stages);
+      mma_commit(smem_u32(done));
     }
-    if (elect_one()) mma_commit(smem_u32(done));
   }
   __syncwarp();
   // ------------------------------------------------------------- epilogue
@@ -467,21 +466,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxPairThreads, 1)
       const uint64_t dsw0 = scale_desc(base + Cfg::SW_OFF), dsx0 = scale_desc(base + Cfg::SX_OFF);
       const uint32_t peer = cluster_addr(base, 1) - base;
       const uint32_t self = cluster_addr(base, 0) - base;
-      Ring r, d;
-      bool ok = true;
-      for (int tile = pair0; tile < p.tiles && ok; tile += pairs) {
-        ok = mbar_wait_cluster(dempty, d.phase ^ 1u, abort_flag, nullptr);
-        d.next(1);
-        for (int kb = 0; kb < p.kblocks; ++kb) {
-          ok = ok && mbar_wait(full + 8 * r.i, r.phase, abort_flag, nullptr);
-          if (!__all_sync(~0u, ok)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t at = r.i * (Cfg::STAGE >> 4);
-          const int steps = min(4, (p.k - kb * kMxBK + 63) >> 6);
-          if (elect_one()) {
+      if (elect_one()) {
+        Ring r, d;
+        bool ok = true;
+        for (int tile = pair0; tile < p.tiles && ok; tile += pairs) {
+          ok = mbar_wait_cluster(dempty, d.phase ^ 1u, abort_flag, nullptr);
+          d.next(1);
+          for (int kb = 0; kb < p.kblocks; ++kb) {
+            ok = ok && mbar_wait(full + 8 * r.i, r.phase, abort_flag, nullptr);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t at = r.i * (Cfg::STAGE >> 4);
+            const int steps = min(4, (p.k - kb * kMxBK + 63) >> 6);
 #pragma unroll
             for (int i = 0; i < NSF; ++i) {
               tmem_copy_scales_pair(sfw + 4 * i, dsw0 + at + i * (kScaleTile >> 4));
@@ -500,17 +496,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxPairThreads, 1)
             }
             mma_commit_pair(empty + self + 8 * r.i);
             mma_commit_pair(empty + peer + 8 * r.i);
+            r.next(S);
           }
-          __syncwarp();
-          r.next(S);
+          if (ok) {
+            mma_commit_pair(dfull + self);
+            mma_commit_pair(dfull + peer);
+          }
         }
-        if (ok && elect_one()) {
-          mma_commit_pair(dfull + self);
-          mma_commit_pair(dfull + peer);
-        }
-        __syncwarp();
+        mma_commit_pair(drain + self);
       }
-      if (elect_one()) mma_commit_pair(drain + self);
       __syncwarp();
       mbar_wait_drain(drain, 0);
     }
