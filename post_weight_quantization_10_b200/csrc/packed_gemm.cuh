@@ -29,7 +29,7 @@ struct PackedGemmArgs {
 };
 
 // Thread roles, by warpgroup:
-//   0    warps 0 and 2: TMA producers, warp 1: MMA issuer
+//   0    warps 0 and 2: TMA producers, warp 1: MMA issuer, warp 3: copies
 //   1..  DG groups of decoders, taking turns by the chunk
 //   then CG groups of consumers: thread = accumulator row, a share of the tokens
 // A chunk costs a decoder a chain of waits, loads, arithmetic, stores and a
@@ -114,13 +114,15 @@ __device__ __forceinline__ void decode_chunk(const PackedGemmArgs& a, const uint
 // Shared-memory addresses of the barriers (arrays of 8-byte words).
 struct PackedBars {
   uint32_t full, empty;            // [stages]: activations and decoded weights there; read
+  uint32_t part;                   // [stages] (C > 1): the part decoded here is there
   uint32_t wfull, wempty;          // [wbufs]: packed chunk there; decoded
   uint32_t rfull, rempty, drain;   // [2]: group finished; added; everything finished
   uint32_t end;
   __device__ PackedBars(uint32_t at, int stages, int wbufs) {
     full = at;
     empty = full + 8 * stages;
-    wfull = empty + 8 * stages;
+    part = empty + 8 * stages;
+    wfull = part + 8 * stages;
     wempty = wfull + 8 * wbufs;
     rfull = wempty + 8 * wbufs;
     rempty = rfull + 16;
@@ -225,7 +227,9 @@ __global__ void __launch_bounds__(PackedCfg<TN, C>::THREADS, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
-      mbar_init(bars.full + 8 * s, 5);  // the activations' producer, four decoder warps
+      // the activations' producer and four decoder warps, or the copying thread
+      mbar_init(bars.full + 8 * s, C > 1 ? 2 : 5);
+      mbar_init(bars.part + 8 * s, 4);
       mbar_init(bars.empty + 8 * s, C);
     }
     for (int i = 0; i < NW; ++i) {
@@ -293,6 +297,25 @@ __global__ void __launch_bounds__(PackedCfg<TN, C>::THREADS, 1)
       if (!ok)
         for (int j = max(0, chunks - NW); j < chunks; ++j)
           mbar_wait_drain(bars.wfull + 8 * (j % NW), (uint32_t)(j / NW) & 1u);
+    } else if (C > 1 && warp == 3 && lane == 0) {
+      // ------------------- copies of the rows decoded here to the other CTA
+      // (8 KB a stage; a decoder that issued them itself lost 800 cycles a chunk)
+      constexpr uint32_t BYTES = Cfg::ROWS * 128;
+      const uint32_t src0 = smem_u32(smem) + Cfg::X_BYTES + part0 * 128;
+      const uint32_t peer = cluster_addr(smem_u32(smem), rank ^ 1) - smem_u32(smem);
+      Ring st;
+      bool ok = true;
+      for (int tile = tile0; tile < a.tiles && ok; tile += tile_step)
+        for (int h = 2 * ch0; h < 2 * ch1; ++h) {
+          if (!mbar_wait(bars.part + 8 * st.i, st.phase, abort_flag, nullptr)) {
+            ok = false;
+            break;
+          }
+          const uint32_t src = src0 + st.i * Cfg::STAGE, bar = bars.full + 8 * st.i;
+          bulk_copy_to_peer(src + peer, src, BYTES, bar + peer);
+          mbar_arrive_expect_tx(bar, BYTES);  // the other CTA's rows
+          st.next(S);
+        }
     } else if (warp == 1) {
       // -------------------------------------------------------- MMA issuer
       if (elect_one()) {
@@ -324,8 +347,6 @@ __global__ void __launch_bounds__(PackedCfg<TN, C>::THREADS, 1)
     for (int c = 0; c < 4; ++c)
       to[c] = smem_u32(smem) + Cfg::X_BYTES + (part0 + row) * 128 +
               ((((q & 1) * 4 + c) ^ (row & 7)) << 4);
-    // C > 1: the other CTA's shared memory, as seen from here
-    const uint32_t peer = C > 1 ? cluster_addr(smem_u32(smem), rank ^ 1) - smem_u32(smem) : 0u;
     for (int tile = tile0; tile < a.tiles && ok; tile += tile_step) {
       const long long row0 = (long long)(tile / a.tiles_m) * 128 + part0;
       const float* zeros = p.zero + (row0 + row) * p.groups;
@@ -390,17 +411,7 @@ __global__ void __launch_bounds__(PackedCfg<TN, C>::THREADS, 1)
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         if (lane < 2) {  // a lane for each of the two stages
-          const uint32_t i = lane ? st1.i : st0.i, bar = bars.full + 8 * i;
-          if (C == 1) {
-            mbar_arrive(bar);
-          } else {
-            // this warp's rows to the other CTA, the other CTA's expected here
-            constexpr uint32_t BYTES = Cfg::STEPS * 8 * 128;
-            const uint32_t src = smem_u32(smem) + i * Cfg::STAGE + Cfg::X_BYTES +
-                                 (part0 + (warp & 3) * Cfg::STEPS * 8) * 128;
-            bulk_copy_to_peer(src + peer, src, BYTES, bar + peer);
-            mbar_arrive_expect_tx(bar, BYTES);
-          }
+          mbar_arrive((C > 1 ? bars.part : bars.full) + 8 * (lane ? st1.i : st0.i));
         } else if (lane == 2 && a.w_tma) {
           mbar_arrive(bars.wempty + 8 * w.i);
         }
