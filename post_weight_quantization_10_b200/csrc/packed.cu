@@ -13,7 +13,7 @@ int packed_gemm_fp16(const PackedArgs& p, cudaStream_t st);  // packed_gemm_fp16
 namespace {
 
 // Tokens that the mma.sync kernel takes.
-constexpr int kFewTokens = 32;
+constexpr int kFewTokens = 16;
 
 template <typename X, int NT, int RT>
 const void* few_kernel(int bits) {
@@ -46,8 +46,7 @@ int launch_few(PackedArgs p, cudaStream_t st) {
   plan.rank_shift = shift;
   const void* kern = one         ? few_kernel<X, 1, 1>(p.bits)
                      : p.m <= 8  ? few_kernel<X, 1, 4>(p.bits)
-                     : p.m <= 16 ? few_kernel<X, 2, 4>(p.bits)
-                                 : few_kernel<X, 4, 4>(p.bits);
+                                 : few_kernel<X, 2, 4>(p.bits);
   CK(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, plan.smem));
   const int grid = one && blocks > 3 * num_sms() ? 3 * num_sms() : blocks;
   cudaLaunchConfig_t lc = {};

@@ -1,4 +1,4 @@
-// packed_few.cuh -- product of a few tokens (at most 32) with packed b-bit
+// packed_few.cuh -- product of a few tokens (at most 16) with packed b-bit
 // codes, on mma.sync.  What bounds it is reading the weights once and turning
 // each code into an operand.
 //
@@ -85,7 +85,7 @@ struct FewPlan {
 // activations in shared memory, which few tokens allow; with more tokens RT = 4
 // reads them from L2 a quarter as often.
 template <typename X, int NT, int RT, int B>
-__global__ void __launch_bounds__(kFewThreads, NT == 4 ? 2 : 3)
+__global__ void __launch_bounds__(kFewThreads, 3)
     k_packed_few(const __grid_constant__ PackedArgs p, const __grid_constant__ FewPlan st) {
   constexpr int ROWS = 16 * RT, KW = 8 / RT;
   extern __shared__ __align__(128) uint8_t smem[];

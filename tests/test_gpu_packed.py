@@ -81,7 +81,8 @@ def test_every_width_and_group(A, bits, group, k):
 @pytest.mark.parametrize("xt", ["bf16", "fp16"])
 @pytest.mark.parametrize("m,n,k,bits,group", [(1, 300, 4096, 3, 128), (20, 200, 2048, 2, 64),
                                               (33, 100, 1056, 5, 32), (200, 300, 1024, 4, 128),
-                                              (600, 700, 4096, 3, 128), (140, 150, 576, 8, 64)])
+                                              (600, 700, 4096, 3, 128), (140, 150, 576, 8, 64),
+                                              (1200, 400, 4096, 4, 128)])
 def test_general_inputs(A, m, n, k, bits, group, xt):
     codes, words, scale, zero = _layer(n, k, bits, group, 7, False)
     rng = np.random.default_rng(8)
@@ -97,6 +98,24 @@ def test_general_inputs(A, m, n, k, bits, group, xt):
         bound = slack + torch.finfo(dt).eps / 2 * np.abs(want) + torch.finfo(dt).tiny
         assert (np.abs(got - want)[fine] <= bound[fine]).all(), dt
         assert (np.abs(want)[~fine] + slack[~fine] >= 65504).all()
+
+
+@pytest.mark.parametrize("xt", ["bf16", "fp16"])
+@pytest.mark.parametrize("m,n,k,bits,group", [(1024, 128, 128, 4, 128), (1025, 300, 1280, 3, 128),
+                                              (1030, 130, 96, 5, 32), (1300, 257, 192, 8, 64),
+                                              (2000, 1, 160, 1, 32), (1024, 513, 320, 2, 64),
+                                              (1111, 70, 256, 6, 128), (1024, 66, 64, 7, 32)])
+def test_many_tokens(A, m, n, k, bits, group, xt):
+    rng = np.random.default_rng(m + n)
+    codes, words, scale, zero = _layer(n, k, bits, group, m, True)
+    x = rng.integers(-2, 3, (m, k)).astype(np.float32)
+    want = torch.from_numpy((x.astype(np.float64) @ mx.packed_weights(words, scale, zero, bits, k).T).astype(np.float32))
+    xd, layer = torch.from_numpy(x).to(DT[xt]).cuda(), _cuda(words, scale, zero)
+    for dt in DT.values():
+        room = torch.full((m * n + 4096,), 3.0, dtype=dt, device="cuda")
+        got = A.packed_matmul(xd, *layer, bits, dt, out=room[:m * n].view(m, n))
+        assert torch.equal(got.cpu(), want.to(dt)), dt
+        assert bool((room[m * n:] == 3.0).all())
 
 
 def test_strided_activations_and_memory_behind(A):
@@ -145,7 +164,7 @@ def test_refusals_on_the_device(A):
 
 
 def test_streams_graphs_and_repeats(A):
-    for m in (1, 24, 160):
+    for m in (1, 24, 160, 1500):
         codes, words, scale, zero = _layer(300, 512, 3, 128, m, False)
         layer = _cuda(words, scale, zero)
         gen = torch.Generator(device="cuda").manual_seed(m)
