@@ -37,6 +37,23 @@ inline bool make_w_map(CUtensorMap* m, const PackedArgs& p, int box_rows) {
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Ranks that share the reduction of a tile, where the tiles are too few.
+inline int split_ranks(long long tiles, int chunks) {
+  int ranks = 1;
+  while (ranks < 8 && chunks >= 4 * ranks && 2 * ranks * tiles <= cluster_ctas(2 * ranks)) ranks *= 2;
+  return ranks;
+}
+
+// About how long a tile shape takes: rounds of tiles x chunks of a rank x a
+// chunk's time, plus what adding partial tiles takes.
+inline double tile_time(const PackedArgs& p, int tokens, int ctas, double chunk_us) {
+  const int chunks = cdiv(p.k, 128);
+  const long long tiles = (long long)cdiv(p.m, tokens) * cdiv(p.n, 128);
+  const int ranks = ctas == 1 ? split_ranks(tiles, chunks) : 1;
+  const int at_once = ranks > 1 ? cluster_ctas(ranks) / ranks : num_sms() / ctas;
+  return (double)((tiles + at_once - 1) / at_once) * cdiv(chunks, ranks) * chunk_us + (ranks > 1 ? 3.0 : 0.0);
+}
+
 template <typename X, int TN, int C, bool BY_BITS>
 int launch_gemm(const PackedArgs& p, cudaStream_t st) {
   using Cfg = PackedCfg<TN, C>;
@@ -49,9 +66,7 @@ int launch_gemm(const PackedArgs& p, cudaStream_t st) {
   a.chunks = cdiv(p.k, 128);
   a.passes = 128 / p.group;
   a.w_tma = p.words % 4 == 0;
-  int ranks = C;
-  if (C == 1)
-    while (ranks < 8 && a.chunks >= 4 * ranks && 2 * ranks * tiles <= cluster_ctas(2 * ranks)) ranks *= 2;
+  int ranks = C == 1 ? split_ranks(tiles, a.chunks) : C;
   // Shared memory: the ranks' partial tiles; packed chunks, which come from HBM,
   // a long way off (a third of the rings, at most 16); operand stages the rest.
   // A decoder group may wait for a buffer that others have yet to use once:
@@ -109,10 +124,16 @@ int launch_gemm(const PackedArgs& p, cudaStream_t st) {
   return ADMMQ_OK;
 }
 
+// The tile shape that is estimated to take least.  A chunk's times are measured
+// (33 tokens of 4096 -> 24576: 47 us in two rounds of 32 chunks; 256: 96 us in
+// three; 4096: 890 us in 21): 64 tokens cost as much as the decoding that they
+// share, 512 a cluster's MMAs.
 template <typename X>
 int packed_gemm(const PackedArgs& p, cudaStream_t st) {
-  if (p.m <= 64) return launch_gemm<X, 64, 1, true>(p, st);
-  if (p.m <= 256) return launch_gemm<X, 128, 1, true>(p, st);
+  const double t64 = tile_time(p, 64, 1, 0.74), t128 = tile_time(p, 128, 1, 1.0),
+               t512 = tile_time(p, 512, 2, 1.32);
+  if (t64 <= t128 && t64 <= t512) return launch_gemm<X, 64, 1, true>(p, st);
+  if (t128 <= t512) return launch_gemm<X, 128, 1, true>(p, st);
   return launch_gemm<X, 256, 2, false>(p, st);
 }
 
