@@ -225,6 +225,25 @@ def test_linear_is_quantize_then_product(A):
             assert torch.equal(y, A.mx_matmul(A.mx_quantize(x, fmt, g), qw, torch.bfloat16))
 
 
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+@pytest.mark.parametrize("m,n,k", [(1, 19300, 2080), (9, 19300, 2048), (5, 300, 12288),
+                                   (100, 19300, 2048), (90, 129, 12320), (400, 3000, 4128)])
+def test_linear_with_more_stages_than_fit(A, fmt, m, n, k):
+    """Many tiles or a long reduction: the stages' ring goes round, activations of
+    few tokens are quantised by a launch of their own.  Against float64 on the
+    dequantised matrices (exact in fp32), and equal to the product's own bits."""
+    gen = torch.Generator(device="cuda").manual_seed(m + n)
+    x = torch.randn((m, k), generator=gen, device="cuda").bfloat16()
+    w = (torch.randn((n, k), generator=gen, device="cuda") * 0.02).bfloat16()
+    g = _dev_g(_g(x)) if fmt == "nvfp4" else None
+    qw, qx = A.mx_quantize(w, fmt), A.mx_quantize(x, fmt, g)
+    y = A.mx_linear(x, qw, torch.float32, tensor_scale=g)
+    assert torch.equal(y, A.mx_matmul(qx, qw, torch.float32))
+    a, b = A.mx_dequantize(qx, torch.float32).double(), A.mx_dequantize(qw, torch.float32).double()
+    bound = (k + 2) * 2.0 ** -23 * (a.abs() @ b.abs().T)
+    assert bool(((y.double() - a @ b.T).abs() <= bound).all())
+
+
 def test_refusals_on_the_device(A):
     x = torch.zeros((4, 64), dtype=torch.bfloat16, device="cuda")
     g = torch.ones(1, device="cuda")
