@@ -380,11 +380,13 @@ def _launch(name: str, device: torch.device, stream, *args):
 
 
 def _empty(shape, dtype, device, stream):
-    """A new tensor that belongs to the stream its kernel runs on."""
+    """A new contiguous tensor of one or two dimensions that belongs to the
+    stream its kernel runs on.  (With strides given, torch takes half the time.)"""
+    strides = (1,) if len(shape) == 1 else (max(shape[1], 1), 1)
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty_strided(shape, strides, dtype=dtype, device=device)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty_strided(shape, strides, dtype=dtype, device=device)
 
 
 def _output(out, shape, dtype, x: torch.Tensor, stream, where: str):
