@@ -10,28 +10,30 @@ using namespace admmq;
 
 namespace {
 
-// A block of threads takes 128 rows x 512 columns: the scale tiles it fills
-// (or reads) are whole and lie next to each other, 2 KB (mxfp4) or 4 KB
-// (nvfp4).  A warp takes a row at a time, a lane 16 elements of it: an nvfp4
-// block, or half of an mxfp4 one, whose two lanes share its largest magnitude.
-constexpr int kSpan = 512;  // columns of a thread block
+// A block of threads takes 128 rows x SPAN columns: the scale tiles it fills (or
+// reads) are whole and lie next to each other.  A lane takes 16 elements: an
+// nvfp4 block, or half of an mxfp4 one, whose two lanes share its largest
+// magnitude.  With 512 columns a warp's accesses are a row's next kilobyte;
+// with 128 it takes four rows at a time, and there are four times the blocks:
+// for matrices that would not fill the SMs (48 x 12288: 8.1 to 5.0 us).
 constexpr int kMxThreads = 256;
-constexpr int kMxWarps = kMxThreads / 32;  // warp w takes rows w, w + 8, ...
+constexpr int kMxWarps = kMxThreads / 32;
 
-template <int FMT, typename T>
+template <int FMT, typename T, int SPAN>
 __global__ void __launch_bounds__(kMxThreads)
     k_mx_quantize(const T* __restrict__ x, long long rows, int k, long long ld, int spans,
                   const float* __restrict__ tensor_scale, uint8_t* __restrict__ codes,
                   uint8_t* __restrict__ scale) {
   constexpr int TILE_K = MxFormat<FMT>::TILE_K;
   constexpr int LANES = MxFormat<FMT>::BLOCK / 16;  // lanes that share a block
-  constexpr int TILES = kSpan / TILE_K;
+  constexpr int TILES = SPAN / TILE_K;
+  constexpr int ROW_LANES = SPAN / 16, ROWS = 32 / ROW_LANES;  // of a warp: lanes of a row, rows
   __shared__ __align__(16) uint8_t tile[TILES * kScaleTile];
   let_next_kernel_start();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const long long row_tile = blockIdx.x / spans;
   const int span = (int)(blockIdx.x - row_tile * spans);
-  const int col = span * kSpan + lane * 16;
+  const int col = span * SPAN + (lane % ROW_LANES) * 16, row0 = warp * ROWS + lane / ROW_LANES;
   const float g = FMT == MX_NVFP4 && tensor_scale ? *tensor_scale : 1.f;
   const float r6g = 1.f / (6.f * g);
   const int col_tiles = (k + TILE_K - 1) / TILE_K;
@@ -42,14 +44,16 @@ __global__ void __launch_bounds__(kMxThreads)
     for (int i = threadIdx.x; i < TILES * kScaleTile / 16; i += kMxThreads)
       reinterpret_cast<uint4*>(tile)[i] = make_uint4(0, 0, 0, 0);
   __syncthreads();
-  const T* src = x + (row_tile * 128 + warp) * ld + col;
-  uint8_t* dst = codes + ((row_tile * 128 + warp) * k + col) / 2;
-  const long long src_step = ld * kMxWarps, dst_step = (long long)(k / 2) * kMxWarps;
-  const int c = lane / LANES;
+  const T* src = x + (row_tile * 128 + row0) * ld + col;
+  uint8_t* dst = codes + ((row_tile * 128 + row0) * k + col) / 2;
+  constexpr int STEP = kMxWarps * ROWS;  // rows from one of a lane's to its next
+  const long long src_step = ld * STEP, dst_step = (long long)(k / 2) * STEP;
+  const int c = lane % ROW_LANES / LANES;
   uint8_t* to = tile + (c >> 2) * kScaleTile + (c & 3);
-  const int n = (last - warp + kMxWarps - 1) / kMxWarps;
-  // a block's lanes are inside or outside together; all stay for the shuffle
-  const bool in = col < k;
+  // rows of the warp's first lane, and of this one; a block's lanes are inside
+  // or outside together, all stay for the shuffle
+  const int n = (last - warp * ROWS + STEP - 1) / STEP;
+  const int mine = col < k ? (last - row0 + STEP - 1) / STEP : 0;
   const bool wide = (((uintptr_t)x | (uintptr_t)(ld * sizeof(T))) & 31) == 0;
   // a few rows' loads go out before the first is used (the rare exact path's
   // branch would keep the compiler from doing so itself)
@@ -60,7 +64,7 @@ __global__ void __launch_bounds__(kMxThreads)
     for (int j = 0; j < AHEAD; ++j) {
 #pragma unroll
       for (int i = 0; i < (int)(4 * sizeof(T)); ++i) raw[j].w[i] = 0u;
-      if (in && j0 + j < n) load_raw(src + j * src_step, wide, raw[j]);
+      if (j0 + j < mine) load_raw(src + j * src_step, wide, raw[j]);
     }
     src += AHEAD * src_step;
 #pragma unroll
@@ -72,9 +76,9 @@ __global__ void __launch_bounds__(kMxThreads)
       if (LANES == 2) amax = max(amax, __shfl_xor_sync(~0u, amax, 1));
       const uint32_t byte = block_scale<FMT>(amax, g, r6g);
       const uint2 out = quantize16<FMT>(v, byte, g);
-      if (in) {
+      if (j0 + j < mine) {
         *reinterpret_cast<uint2*>(dst) = out;
-        if (lane % LANES == 0) to[scale_at((j0 + j) * kMxWarps + warp, 0)] = (uint8_t)byte;
+        if (lane % LANES == 0) to[scale_at((j0 + j) * STEP + row0, 0)] = (uint8_t)byte;
       }
       dst += dst_step;
     }
@@ -85,19 +89,20 @@ __global__ void __launch_bounds__(kMxThreads)
     out[i] = reinterpret_cast<const uint4*>(tile)[i];
 }
 
-template <int FMT, typename T>
+template <int FMT, typename T, int SPAN>
 __global__ void __launch_bounds__(kMxThreads)
     k_mx_dequantize(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scale,
                     long long rows, int k, int spans, const float* __restrict__ tensor_scale,
                     T* __restrict__ out, long long ld) {
   constexpr int TILE_K = MxFormat<FMT>::TILE_K;
   constexpr int LANES = MxFormat<FMT>::BLOCK / 16;
-  constexpr int TILES = kSpan / TILE_K;
+  constexpr int TILES = SPAN / TILE_K;
+  constexpr int ROW_LANES = SPAN / 16, ROWS = 32 / ROW_LANES;  // of a warp: lanes of a row, rows
   __shared__ __align__(16) uint8_t tile[TILES * kScaleTile];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const long long row_tile = blockIdx.x / spans;
   const int span = (int)(blockIdx.x - row_tile * spans);
-  const int col = span * kSpan + lane * 16;
+  const int col = span * SPAN + (lane % ROW_LANES) * 16, row0 = warp * ROWS + lane / ROW_LANES;
   const float g = FMT == MX_NVFP4 && tensor_scale ? *tensor_scale : 1.f;
   const int col_tiles = (k + TILE_K - 1) / TILE_K;
   const int here = min(TILES, col_tiles - span * TILES);
@@ -108,11 +113,12 @@ __global__ void __launch_bounds__(kMxThreads)
   __syncthreads();
   if (col >= k) return;
   const int last = rows - row_tile * 128 < 128 ? (int)(rows - row_tile * 128) : 128;
-  const int n = (last - warp + kMxWarps - 1) / kMxWarps;
-  const uint8_t* src = codes + ((row_tile * 128 + warp) * k + col) / 2;
-  T* dst = out + (row_tile * 128 + warp) * ld + col;
-  const long long src_step = (long long)(k / 2) * kMxWarps, dst_step = ld * kMxWarps;
-  const int c = lane / LANES;
+  constexpr int STEP = kMxWarps * ROWS;
+  const int n = (last - row0 + STEP - 1) / STEP;
+  const uint8_t* src = codes + ((row_tile * 128 + row0) * k + col) / 2;
+  T* dst = out + (row_tile * 128 + row0) * ld + col;
+  const long long src_step = (long long)(k / 2) * STEP, dst_step = ld * STEP;
+  const int c = lane % ROW_LANES / LANES;
   const uint8_t* from = tile + (c >> 2) * kScaleTile + (c & 3);
   const bool wide = (((uintptr_t)out | (uintptr_t)(ld * sizeof(T))) & 31) == 0;
   constexpr int AHEAD = 8;
@@ -125,7 +131,7 @@ __global__ void __launch_bounds__(kMxThreads)
 #pragma unroll
     for (int j = 0; j < AHEAD; ++j) {
       if (j0 + j >= n) break;
-      const float t = block_step<FMT>(from[scale_at((j0 + j) * kMxWarps + warp, 0)], g);
+      const float t = block_step<FMT>(from[scale_at((j0 + j) * STEP + row0, 0)], g);
       float v[16];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
@@ -369,11 +375,14 @@ int admmq_mx_quantize(const void* x, int x_dtype, int64_t rows, int k, int64_t l
     return ADMMQ_ERR_INVALID_ARG;
   int rc = device_ok();
   if (rc) return rc;
-  const int spans = cdiv(k, kSpan);
-  const long long grid = (rows + 127) / 128 * spans;
+  const long long row_tiles = (rows + 127) / 128;
+  const bool small = row_tiles * cdiv(k, 512) < 2 * num_sms();
+  const int spans = cdiv(k, small ? 128 : 512);
+  const long long grid = row_tiles * spans;
   if (grid > 0x7FFFFFFFll) return ADMMQ_ERR_UNSUPPORTED;
-#define QUANTIZE(FMT, T)                                                                         \
-  count_launch(), k_mx_quantize<FMT, T><<<(unsigned)grid, kMxThreads, 0, (cudaStream_t)stream>>>( \
+#define QUANTIZE(FMT, T)                                                                        \
+  auto kern = small ? k_mx_quantize<FMT, T, 128> : k_mx_quantize<FMT, T, 512>;                  \
+  count_launch(), kern<<<(unsigned)grid, kMxThreads, 0, (cudaStream_t)stream>>>(                \
                       (const T*)x, rows, k, ld, spans, tensor_scale, codes, scale)
   MX_DISPATCH(fmt, x_dtype, QUANTIZE)
 #undef QUANTIZE
@@ -393,13 +402,15 @@ int admmq_mx_dequantize(const uint8_t* codes, const uint8_t* scale, int64_t rows
     return ADMMQ_ERR_INVALID_ARG;
   int rc = device_ok();
   if (rc) return rc;
-  const int spans = cdiv(k, kSpan);
-  const long long grid = (rows + 127) / 128 * spans;
+  const long long row_tiles = (rows + 127) / 128;
+  const bool small = row_tiles * cdiv(k, 512) < 2 * num_sms();
+  const int spans = cdiv(k, small ? 128 : 512);
+  const long long grid = row_tiles * spans;
   if (grid > 0x7FFFFFFFll) return ADMMQ_ERR_UNSUPPORTED;
-#define DEQUANTIZE(FMT, T)                                                                     \
-  count_launch(),                                                                              \
-      k_mx_dequantize<FMT, T><<<(unsigned)grid, kMxThreads, 0, (cudaStream_t)stream>>>(        \
-          codes, scale, rows, k, spans, tensor_scale, (T*)out, ld)
+#define DEQUANTIZE(FMT, T)                                                                      \
+  auto kern = small ? k_mx_dequantize<FMT, T, 128> : k_mx_dequantize<FMT, T, 512>;              \
+  count_launch(), kern<<<(unsigned)grid, kMxThreads, 0, (cudaStream_t)stream>>>(                \
+                      codes, scale, rows, k, spans, tensor_scale, (T*)out, ld)
   MX_DISPATCH(fmt, out_dtype, DEQUANTIZE)
 #undef DEQUANTIZE
   CK(cudaGetLastError());
