@@ -58,6 +58,15 @@ __device__ __forceinline__ uint32_t idesc_mx(int M, int N, uint32_t sf) {
          (FMT == MX_MXFP4 ? 1u << 23 : 0u) | ((uint32_t)(M >> 7) << 27) | (sf << 29);
 }
 
+// The tensor scales as two factors of a sum, applied one after the other: their
+// product and 1, or, where the product alone leaves fp32's normal range and the
+// sum may bring it back, the larger and the smaller.
+__device__ __forceinline__ float2 output_factors(const float* gw, const float* gx) {
+  const float a = gw ? *gw : 1.f, b = gx ? *gx : 1.f, g = a * b;
+  const bool left = (g < 0x1p-126f && a > 0.f && b > 0.f) || g == __int_as_float(0x7F800000);
+  return left ? make_float2(fmaxf(a, b), fminf(a, b)) : make_float2(g, 1.f);
+}
+
 __device__ __forceinline__ void put(float* p, float v) { *p = v; }
 __device__ __forceinline__ void put(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 __device__ __forceinline__ void put(__half* p, float v) { *p = __float2half_rn(v); }
@@ -85,29 +94,51 @@ struct MxArgs {
 constexpr int kMxBK = 256;  // elements of K per stage: 128-byte rows
 constexpr int kMxTileThreads = 192;
 
-// One warp quantises 256 columns from `col` of one row: as k_mx_quantize does,
-// into a stage's swizzled code rows and its scale tiles.  What lies behind the
-// last column is zero (codes and scales).
+// Quantises a block's part of the activations, tokens x 256-column stages from
+// kb0 on, as k_mx_quantize does, into the stages' swizzled code rows and scale
+// tiles.  Half a warp takes a token's stage (16 columns a lane) and loads a few
+// of them before it uses the first.  What lies behind the last column is zero
+// (codes and scales).
 template <int FMT, typename X>
-__device__ __forceinline__ void quantize_into(const X* x, int k, int col, int row, float g, float r6g,
-                                              uint8_t* codes, uint8_t* scales) {
-  constexpr int LANES = MxFormat<FMT>::BLOCK / 16;
-  const int lane = threadIdx.x & 31;
-  if (lane >= 16) return;   // sixteen elements a lane
-  const bool in = col + 16 * lane < k;
-  Raw16<X> raw;
+__device__ __forceinline__ void quantize_stages(const X* x, long long ld, int tokens, int k, int kb0,
+                                                int stages, const float* tensor_scale, uint8_t* smem,
+                                                int stage_bytes, int x_off, int sx_off, int warp) {
+  constexpr int LANES = MxFormat<FMT>::BLOCK / 16, AHEAD = 8 / (int)sizeof(X);
+  const float g = tensor_scale ? *tensor_scale : 1.f, r6g = 1.f / (6.f * g);
+  const int half = (threadIdx.x >> 4) & 1, lane = threadIdx.x & 15, items = tokens * stages;
+  for (int i0 = 2 * warp; i0 < items; i0 += 8 * AHEAD) {
+    Raw16<X> raw[AHEAD];
+    int token[AHEAD], stage[AHEAD];
 #pragma unroll
-  for (int i = 0; i < (int)(4 * sizeof(X)); ++i) raw.w[i] = 0u;
-  if (in) load_raw(x + col + 16 * lane, false, raw);
-  float v[16];
-  values_of(raw, v);
-  uint32_t amax = amax_of(raw);
-  if (LANES == 2) amax = max(amax, __shfl_xor_sync(0xFFFFu, amax, 1));
-  const uint32_t byte = in ? block_scale<FMT>(amax, g, r6g) : 0u;
-  const uint2 out = quantize16<FMT>(v, byte, g);
-  *reinterpret_cast<uint2*>(codes + row * 128 + (((lane >> 1) ^ (row & 7)) << 4) + 8 * (lane & 1)) = out;
-  const int c = lane / LANES;
-  if (lane % LANES == 0) scales[(c >> 2) * kScaleTile + scale_at(row, c & 3)] = (uint8_t)byte;
+    for (int j = 0; j < AHEAD; ++j) {
+      const int i = i0 + 8 * j + half;
+      stage[j] = i / tokens;
+      token[j] = i - stage[j] * tokens;
+      const int col = (kb0 + stage[j]) * kMxBK + 16 * lane;
+#pragma unroll
+      for (int w = 0; w < (int)(4 * sizeof(X)); ++w) raw[j].w[w] = 0u;
+      if (i < items && col < k) load_raw(x + token[j] * ld + col, false, raw[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < AHEAD; ++j) {
+      if (i0 + 8 * j >= items) break;
+      const int row = token[j];
+      const bool in = (kb0 + stage[j]) * kMxBK + 16 * lane < k;
+      float v[16];
+      values_of(raw[j], v);
+      uint32_t amax = amax_of(raw[j]);
+      if (LANES == 2) amax = max(amax, __shfl_xor_sync(~0u, amax, 1));
+      const uint32_t byte = in ? block_scale<FMT>(amax, g, r6g) : 0u;
+      const uint2 out = quantize16<FMT>(v, byte, g);
+      if (i0 + 8 * j + half < items) {
+        uint8_t *codes = smem + stage[j] * stage_bytes + x_off, *scales = smem + stage[j] * stage_bytes + sx_off;
+        *reinterpret_cast<uint2*>(codes + row * 128 + (((lane >> 1) ^ (row & 7)) << 4) + 8 * (lane & 1)) = out;
+        const int c = lane / LANES;
+        if (lane % LANES == 0) scales[(c >> 2) * kScaleTile + scale_at(row, c & 3)] = (uint8_t)byte;
+      }
+      __syncwarp();
+    }
+  }
 }
 
 // One output tile of 128 columns x tn tokens per cluster; the cluster's CTAs
@@ -117,6 +148,13 @@ __device__ __forceinline__ void quantize_into(const X* x, int k, int col, int ro
 // FUSED (a few tokens, every stage of a block resident): the activations are
 // quantised here, by the epilogue's warps while the weights are on their way,
 // instead of by a launch of their own.
+// What bounds it: up to 128 tokens the weights (0.53 bytes each) are all that
+// counts, and a layer's 9 to 30 MB are so little that the chain load - MMA -
+// cluster sum shows: 1 token of 4096 -> 4096 5.6 us device time where HBM needs
+// 1.4, 48 tokens of 12288 -> 4096 15.6 us (quantisation included) of 4.6.  The
+// cluster's share of k was worth most (48 tokens: 36 to 24 us), then having all
+// of a block's stages in flight at once, then overlapping with the quantisation
+// in front (24 to 19) or, for a few tokens, doing it here (1 token: 9.3 to 5.6).
 //   warp 0  TMA producer    warp 1  MMA issuer    warps 2-5  epilogue
 template <int FMT, typename T, bool FUSED>
 __global__ void __launch_bounds__(kMxTileThreads)
@@ -255,25 +293,20 @@ __global__ void __launch_bounds__(kMxTileThreads)
   bool ok = true;
   const long long col = (long long)tn_tile * 128 + row;
   const int tokens = min(p.tn, p.m - tm_tile * p.tn);
-  const float g = (p.gw ? *p.gw : 1.f) * (p.gx ? *p.gx : 1.f);
+  const float2 g = output_factors(p.gw, p.gx);
   T* out = reinterpret_cast<T*>(p.out) + (long long)tm_tile * p.tn * p.n + col;
   const int per = (tokens + (int)ranks - 1) / (int)ranks;  // tokens that a rank sums
   const uint32_t part = smem_u32(smem) + p.stages * p.stage_bytes;  // [ranks][per][128]
   if (FUSED && warp >= 2) {
-    const float gx = p.gx ? *p.gx : 1.f, r6g = 1.f / (6.f * gx);
-    const int items = p.m * (kb1 - kb0);
-    for (int i = warp - 2; i < items; i += 4) {
-      const int s = i / p.m, token = i - s * p.m, c = (kb0 + s) * kMxBK;
-      uint8_t* st = smem + s * p.stage_bytes;
-      const long long at = token * p.ld;
-      if (p.raw_dtype == ADMMQ_DTYPE_BF16)
-        quantize_into<FMT>((const __nv_bfloat16*)p.raw + at, p.k, c, token, gx, r6g, st + x_off, st + sx_off);
-      else if (p.raw_dtype == ADMMQ_DTYPE_F16)
-        quantize_into<FMT>((const __half*)p.raw + at, p.k, c, token, gx, r6g, st + x_off, st + sx_off);
-      else
-        quantize_into<FMT>((const float*)p.raw + at, p.k, c, token, gx, r6g, st + x_off, st + sx_off);
-      __syncwarp();
-    }
+    auto quantise = [&](auto* x) {
+      quantize_stages<FMT>(x, p.ld, p.m, p.k, kb0, kb1 - kb0, p.gx, smem, p.stage_bytes, x_off, sx_off, warp - 2);
+    };
+    if (p.raw_dtype == ADMMQ_DTYPE_BF16)
+      quantise((const __nv_bfloat16*)p.raw);
+    else if (p.raw_dtype == ADMMQ_DTYPE_F16)
+      quantise((const __half*)p.raw);
+    else
+      quantise((const float*)p.raw);
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(quantised));
@@ -298,7 +331,7 @@ __global__ void __launch_bounds__(kMxTileThreads)
             ++owner;
           }
         } else if (col < p.n) {
-          put(out + (long long)(c + i) * p.n, v[i] * g);
+          put(out + (long long)(c + i) * p.n, v[i] * g.x * g.y);
         }
       }
     }
@@ -315,7 +348,7 @@ __global__ void __launch_bounds__(kMxTileThreads)
         float v = 0.f;
         for (uint32_t r = 0; r < ranks; ++r)
           v += ld_shared_f32(part + (((int)r * per + c - c0) * 128 + row) * 4);
-        put(out + (long long)c * p.n, v * g);
+        put(out + (long long)c * p.n, v * g.x * g.y);
       }
     }
   }
@@ -382,6 +415,9 @@ struct MxPairCfg {
 // columns; a second accumulator would leave no room for the scales).  The
 // epilogue takes the whole accumulator into registers, frees it for the next
 // tile's MMAs and stores from there.
+// What bounds it: the tensor cores under the power limit.  4096 tokens of
+// 4096 -> 24576 in mxfp4: 173 us with the quantisation, 4.8 PFLOP/s (1.58 GHz at
+// 985 W); single CTAs with 128 x 256 tiles took 581 us.
 //   warp 0  TMA producer    warp 1  MMA issuer    warps 2-9  epilogue
 template <int FMT, typename T>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxPairThreads, 1)
@@ -511,7 +547,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxPairThreads, 1)
   } else {
     const int half = (warp - 2) >> 2, quarter = warp & 3;
     const uint32_t ta = tmem + ((uint32_t)(quarter * 32) << 16) + half * 128;
-    const float g = (p.gw ? *p.gw : 1.f) * (p.gx ? *p.gx : 1.f);
+    const float2 g = output_factors(p.gw, p.gx);
     const uint32_t dempty0 = cluster_addr(dempty, 0);
     Ring d;
     bool ok = true;
@@ -543,7 +579,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxPairThreads, 1)
         T* out = reinterpret_cast<T*>(p.out) + (long long)token0 * p.n + col;
 #pragma unroll
         for (int i = 0; i < 128; ++i) {
-          if (i < tokens) put(out, v[i] * g);
+          if (i < tokens) put(out, v[i] * g.x * g.y);
           out += p.n;
         }
       }

@@ -298,3 +298,37 @@ def test_streams_graphs_and_repeats(A):
                     graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(graphs[0][2], want) and torch.equal(graphs[1][2], want2)
+
+
+@pytest.mark.parametrize("tokens", [8, 128, 256])
+@pytest.mark.parametrize("element,byte,g", [(6.0, 0x7E, 2.0**-77), (0.5, 0x01, 2.0**66)])
+def test_tensor_scales_whose_product_leaves_the_range(A, tokens, element, byte, g):
+    """The output is representable, the product of the tensor scales is not:
+    a^2 k with a = element x block scale, a whole multiple of a power of two
+    (2688^2 = 441 x 2^14), exact in fp32, times two scales of 2^-77 and 2^-78
+    (2^-155) or 2^66 each (2^132)."""
+    k, n = 1024, 256
+    step = 448.0 if byte == 0x7E else 2.0**-9
+    ga, gb = (2.0**-77, 2.0**-78) if g < 1 else (g, g)
+    code = 7 if element == 6.0 else 1
+
+    def tensor(rows, gg):
+        tiles = torch.full((-(-rows // 128) * (k // 64) * 512,), byte, dtype=torch.uint8, device="cuda")
+        codes = torch.full((rows, k // 2), 17 * code, dtype=torch.uint8, device="cuda")
+        return A.MxTensor(codes, tiles, "nvfp4", _dev_g(gg))
+
+    want = (element * step) ** 2 * k * ga * gb
+    assert float(np.float32(want)) == want
+    w = tensor(n, gb)
+    if tokens == 8:
+        # quantised on the way in: largest element 6, block scale 448 or 2^-9
+        # (an element of 6 keeps that block scale; the others are 1/2)
+        x = torch.full((tokens, k), element * step * ga, dtype=torch.float32, device="cuda")
+        if byte == 0x01:
+            x[:, ::16] = 6 * step * ga
+            want *= (1 + 11 / 16)
+        y = A.mx_linear(x, w, torch.float32, tensor_scale=_dev_g(ga))
+    else:
+        y = A.mx_matmul(tensor(tokens, ga), w, torch.float32)
+    assert y.shape == (tokens, n)
+    assert torch.equal(y.cpu(), torch.full((tokens, n), want, dtype=torch.float32))
