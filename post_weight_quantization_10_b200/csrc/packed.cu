@@ -12,8 +12,12 @@ int packed_gemm_fp16(const PackedArgs& p, cudaStream_t st);  // packed_gemm_fp16
 
 namespace {
 
-// Tokens that the mma.sync kernel takes.
-constexpr int kFewTokens = 16;
+// Tokens that the mma.sync kernel takes: up to there it is the faster one for
+// most layers, beyond it the tensor-memory kernel.  In us, mma.sync against
+// tcgen05: 9 to 12 tokens of 4096 -> 4096 (4 bits) 12.2 / 13.3, 4096 -> 6144 (3)
+// 14.5 / 18.1, 4096 -> 24576 (4) 45 / 55, 12288 -> 4096 (2) 27 / 22.7; 16 tokens
+// 15.5 / 13.2, 17.8 / 18.3, 59 / 48, 28 / 22.9.
+constexpr int kFewTokens = 12;
 
 template <typename X, int NT, int RT>
 const void* few_kernel(int bits) {
@@ -31,9 +35,11 @@ int launch_few(PackedArgs p, cudaStream_t st) {
   // all activations next to two stages in a third of the shared memory?
   const bool one = p.m <= 8 && (long long)p.m * (spans * 256 + 64) <= 34 * 1024;
   const int rows = one ? 16 : 64, blocks = cdiv(p.n, rows);
+  // ranks, as long as all blocks run at once, three on an SM (a fourth block's
+  // worth: 4 tokens of 12288 -> 4096 20.9 us instead of 14.6)
   int ranks = 1, shift = 0;
   if (!one)
-    while (ranks < 8 && blocks * 2 * ranks <= 4 * num_sms() && spans >= 4 * ranks) ranks *= 2, ++shift;
+    while (ranks < 8 && blocks * 2 * ranks <= 3 * num_sms() && spans >= 4 * ranks) ranks *= 2, ++shift;
   const int range = cdiv(spans, ranks), most = one ? 32 : 8;
   int per = 1;
   while (per < most && per < range) per *= 2;
