@@ -45,7 +45,7 @@ def _cuda(words, scale, zero):
 
 SHAPES = [(1, 1, 128), (1, 130, 256), (2, 33, 128), (3, 640, 4096), (8, 17, 384), (9, 100, 640),
           (16, 257, 512), (17, 64, 1152), (33, 384, 256), (64, 129, 1024), (65, 200, 128),
-          (129, 260, 384), (300, 520, 640)]
+          (129, 260, 384), (300, 520, 640), (12, 515, 2048), (13, 64, 640)]
 
 
 @pytest.mark.parametrize("xt", ["bf16", "fp16"])
