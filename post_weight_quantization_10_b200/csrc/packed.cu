@@ -44,7 +44,7 @@ int launch_few(PackedArgs p, cudaStream_t st) {
   int per = 1;
   while (per < most && per < range) per *= 2;
   FewPlan plan(rows, per, range, p.bits, p.group, p.m, !one);
-  while (plan.smem > 72 * 1024 && per > 1) {
+  while (plan.smem > (one ? 110 : 72) * 1024 && per > 1) {
     per /= 2;
     plan = FewPlan(rows, per, range, p.bits, p.group, p.m, !one);
   }
@@ -54,7 +54,7 @@ int launch_few(PackedArgs p, cudaStream_t st) {
                      : p.m <= 8  ? few_kernel<X, 1, 4>(p.bits)
                                  : few_kernel<X, 2, 4>(p.bits);
   CK(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, plan.smem));
-  const int grid = one && blocks > 3 * num_sms() ? 3 * num_sms() : blocks;
+  const int once = few_blocks(1) * num_sms(), grid = one && blocks > once ? once : blocks;
   cudaLaunchConfig_t lc = {};
   lc.gridDim = dim3((unsigned)(grid * ranks));
   lc.blockDim = dim3(kFewThreads);

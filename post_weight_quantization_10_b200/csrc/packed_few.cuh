@@ -21,6 +21,12 @@
 namespace admmq {
 
 constexpr int kFewThreads = 256;
+// Blocks on an SM.  With RT = 1 two: their longer stages and registers for two
+// rows' codes are worth more than a third block (4096 -> 4096 at 4 bits: 1 token
+// 5.7 us against 6.7, 4 tokens 6.6 / 7.9; 4096 -> 24576 22.3 / 24.3 and 23.6 /
+// 26.0; only 384 row blocks, one round of three, lose: 4096 -> 6144 7.8 / 7.4).
+// With RT = 4 three (8 tokens of 4096 -> 24576 36 us, with two 51).
+constexpr int few_blocks(int rt) { return rt == 1 ? 2 : 3; }
 
 template <typename X>
 __device__ __forceinline__ void mma_m16n8k16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
@@ -87,7 +93,7 @@ struct FewPlan {
 // activations in shared memory, which few tokens allow; with more tokens RT = 4
 // reads them from L2 a quarter as often.
 template <typename X, int NT, int RT, int B>
-__global__ void __launch_bounds__(kFewThreads, 3)
+__global__ void __launch_bounds__(kFewThreads, few_blocks(RT))
     k_packed_few(const __grid_constant__ PackedArgs p, const __grid_constant__ FewPlan st) {
   constexpr int ROWS = 16 * RT, KW = 8 / RT;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -199,6 +205,8 @@ __global__ void __launch_bounds__(kFewThreads, 3)
   fetch_next(0);
   fetch_next(1);
   if (!st.x_staged) fetch_x(sp0, sp1 - sp0, 0);
+  const bool by_threads = !vec || !vec_s || st.x_staged;
+  if (!by_threads) __syncthreads();
   bool ok = true;
   int buf = 0;
   uint32_t phase = 0;
@@ -214,7 +222,8 @@ __global__ void __launch_bounds__(kFewThreads, 3)
       if (st.x_staged) fetch_x(sp, there, buf);
       asm volatile("cp.async.wait_group 1;" ::: "memory");
       ok = mbar_wait(smem_u32(&full[buf]), phase, &abort_flag, nullptr) && ok;
-      __syncthreads();
+      // what threads stored themselves, unlike bulk copies, waits for all of them
+      if (by_threads) __syncthreads();
       const uint8_t* base = smem + buf * st.bytes;
       const uint32_t* src =
           reinterpret_cast<const uint32_t*>(base) + (rt * 16 + r) * st.pitch + (4 * kw + q) * B;
