@@ -16,6 +16,10 @@ namespace {
 // magnitude.  With 512 columns a warp's accesses are a row's next kilobyte;
 // with 128 it takes four rows at a time, and there are four times the blocks:
 // for matrices that would not fill the SMs (48 x 12288: 8.1 to 5.0 us).
+// What bounds them: HBM for 16-bit to mxfp4 (24576 x 4096 in about 40 us, 6.2 TB/s)
+// and for dequantisation (25600 x 5120 nvfp4 to bf16 57 us, 5.9 TB/s of 6.5); for
+// nvfp4 the conversions to e2m1, a few lanes a clock and SM, which every element
+// takes twice (see quantize16): 2047 x 12288 in 24 us, HBM would need 10.
 constexpr int kMxThreads = 256;
 constexpr int kMxWarps = kMxThreads / 32;
 

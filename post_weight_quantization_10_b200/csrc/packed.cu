@@ -14,9 +14,9 @@ namespace {
 
 // Tokens that the mma.sync kernel takes: up to there it is the faster one for
 // most layers, beyond it the tensor-memory kernel.  In us, mma.sync against
-// tcgen05: 9 to 12 tokens of 4096 -> 4096 (4 bits) 12.2 / 13.3, 4096 -> 6144 (3)
-// 14.5 / 18.1, 4096 -> 24576 (4) 45 / 55, 12288 -> 4096 (2) 27 / 22.7; 16 tokens
-// 15.5 / 13.2, 17.8 / 18.3, 59 / 48, 28 / 22.9.
+// tcgen05: 9 to 12 tokens of 4096 -> 4096 (4 bits) 11.0 / 13.3, 4096 -> 6144 (3)
+// 13.5 / 18.1, 4096 -> 24576 (4) 40 / 55, 12288 -> 4096 (2) 24.1 / 22.7; 16 tokens
+// 13.1 / 13.2, 16.1 / 18.3, 52 / 48, 24.4 / 22.9.
 constexpr int kFewTokens = 12;
 
 template <typename X, int NT, int RT>
@@ -32,8 +32,10 @@ const void* few_kernel(int bits) {
 template <typename X>
 int launch_few(PackedArgs p, cudaStream_t st) {
   const int spans = cdiv(p.k, 128);
-  // all activations next to two stages in a third of the shared memory?
-  const bool one = p.m <= 8 && (long long)p.m * (spans * 256 + 64) <= 34 * 1024;
+  // all activations next to two stages in half of the shared memory? (8 tokens of
+  // 4096 -> 24576 at 3 bits: 28.9 us against 31.6 staged, 6 tokens 24.5 / 31.0; 2 of
+  // 12288 -> 4096 13.3 / 12.6)
+  const bool one = p.m <= 8 && (long long)p.m * (spans * 256 + 64) <= 70 * 1024;
   const int rows = one ? 16 : 64, blocks = cdiv(p.n, rows);
   // ranks, as long as all blocks run at once, three on an SM (a fourth block's
   // worth: 4 tokens of 12288 -> 4096 20.9 us instead of 14.6)

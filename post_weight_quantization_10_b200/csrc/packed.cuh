@@ -85,7 +85,10 @@ __device__ __forceinline__ void decode32(const uint32_t (&w)[B], float zero, uin
     }
 #pragma unroll
     for (int c0 = 0; c0 < 16; c0 += PER) {
-      const uint32_t t = __byte_perm(bits_at<B>(w, B * c0), bits_at<B>(w, B * (c0 + 16)), 0x5410);
+      // (a window that ends with its word is that word's upper half)
+      const bool upper = (B * c0 & 31) == 16 && (B * 16 & 31) == 0;
+      const uint32_t t = upper ? __byte_perm(w[B * c0 >> 5], w[B * (c0 + 16) >> 5], 0x7632)
+                               : __byte_perm(bits_at<B>(w, B * c0), bits_at<B>(w, B * (c0 + 16)), 0x5410);
 #pragma unroll
       for (int i = 0; i < PER; ++i) {
         if (c0 + i >= 16) break;

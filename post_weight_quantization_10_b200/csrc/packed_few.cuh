@@ -2,7 +2,8 @@
 // codes, on mma.sync.  What bounds it is reading the weights once and turning
 // each code into an operand: about two instructions a code pair, which no more
 // tokens make more, and for small layers the chain launch - load - decode - sum
-// (1 token of 4096 -> 6144 at 3 bits: 7.4 us device time, HBM needs 1.7).
+// (1 token of 4096 -> 6144 at 3 bits: 7.6 us device time, HBM needs 1.7;
+// of 4096 -> 24576 at 4 bits 21 of 8).
 //
 // mma.m16n8k16 sums over k in an order that nothing depends on, so each of the
 // four lanes that share a weight row takes 32 consecutive codes of a
@@ -122,10 +123,14 @@ __global__ void __launch_bounds__(kFewThreads, few_blocks(RT))
     const int g0 = sp * passes, groups = min(st.groups, p.groups - g0);
     const int t = threadIdx.x;
     if (t == 0)
-      mbar_arrive_expect_tx(bar, rows * ((vec ? words * 4 : 0) + (vec_s ? groups * 8 : 0)));
+      mbar_arrive_expect_tx(bar, rows * ((vec ? words * 4 : 0) + (vec_s && !st.x_staged ? groups * 8 : 0)));
+    // (a row's copies are issued by a thread each, a few in every warp: one warp
+    // that issued all of them would be late for the products)
+    constexpr int MINE = ROWS / (kFewThreads / 32);
+    const int row = warp * MINE + lane % MINE;
     if (vec) {
-      if (t < rows)
-        bulk_load(base + t * st.pitch * 4, p.packed + (row0 + t) * p.words + first, words * 4, bar);
+      if (lane < MINE && row < rows)
+        bulk_load(base + row * st.pitch * 4, p.packed + (row0 + row) * p.words + first, words * 4, bar);
     } else {
       for (int row = warp; row < rows; row += kFewThreads / 32)
         for (int c = lane; c < words; c += 32)
@@ -133,13 +138,20 @@ __global__ void __launch_bounds__(kFewThreads, few_blocks(RT))
                             p.packed + (row0 + row) * p.words + first + c, true);
     }
     const uint32_t s_dst = base + st.s_off, z_dst = s_dst + ROWS * st.groups * 4;
-    if (vec_s) {
-      const int row = t - 64;
-      if (row >= 0 && row < rows)
-        bulk_load(s_dst + row * st.groups * 4, p.scale + (row0 + row) * p.groups + g0, groups * 4, bar);
-      if (row >= 64 && row - 64 < rows)
-        bulk_load(z_dst + (row - 64) * st.groups * 4, p.zero + (row0 + row - 64) * p.groups + g0,
-                  groups * 4, bar);
+    if (vec_s && st.x_staged) {
+      const int shift = __ffs(st.groups) - 3;  // of 16-byte pieces
+      for (int i = t; i < ROWS << shift; i += kFewThreads) {
+        const int r16 = i >> shift, c = (i & ((1 << shift) - 1)) * 4;
+        if (r16 < rows && c < groups) {
+          const long long at = (row0 + r16) * p.groups + g0 + c;
+          cp_async16(s_dst + i * 16, p.scale + at);
+          cp_async16(z_dst + i * 16, p.zero + at);
+        }
+      }
+    } else if (vec_s) {
+      if (lane >= MINE && lane < 3 * MINE && row < rows)
+        bulk_load((lane < 2 * MINE ? s_dst : z_dst) + row * st.groups * 4,
+                  (lane < 2 * MINE ? p.scale : p.zero) + (row0 + row) * p.groups + g0, groups * 4, bar);
     } else {
       const int shift = __ffs(st.groups) - 1;
       for (int i = t; i < ROWS << shift; i += kFewThreads) {
@@ -222,7 +234,7 @@ __global__ void __launch_bounds__(kFewThreads, few_blocks(RT))
       if (st.x_staged) fetch_x(sp, there, buf);
       asm volatile("cp.async.wait_group 1;" ::: "memory");
       ok = mbar_wait(smem_u32(&full[buf]), phase, &abort_flag, nullptr) && ok;
-      // what threads stored themselves, unlike bulk copies, waits for all of them
+      // what threads stored or copied themselves, unlike bulk copies, waits for all
       if (by_threads) __syncthreads();
       const uint8_t* base = smem + buf * st.bytes;
       const uint32_t* src =
