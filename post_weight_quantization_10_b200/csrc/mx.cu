@@ -15,11 +15,13 @@ namespace {
 // nvfp4 block, or half of an mxfp4 one, whose two lanes share its largest
 // magnitude.  With 512 columns a warp's accesses are a row's next kilobyte;
 // with 128 it takes four rows at a time, and there are four times the blocks:
-// for matrices that would not fill the SMs (48 x 12288: 8.1 to 5.0 us).
+// for matrices of less than four blocks an SM (there and back, 512 against 128
+// columns: 48 x 12288 8.1 / 5.0 us to quantise, 2047 x 12288 37.7 / 35.0; but
+// 24576 x 4096 85.5 / 89.0, 25600 x 5120 dequantised 60 / 64).
 // What bounds them: HBM for 16-bit to mxfp4 (24576 x 4096 in about 40 us, 6.2 TB/s)
 // and for dequantisation (25600 x 5120 nvfp4 to bf16 57 us, 5.9 TB/s of 6.5); for
 // nvfp4 the conversions to e2m1, a few lanes a clock and SM, which every element
-// takes twice (see quantize16): 2047 x 12288 in 24 us, HBM would need 10.
+// takes twice (see quantize16): 2047 x 12288 in 23 us, HBM would need 10.
 constexpr int kMxThreads = 256;
 constexpr int kMxWarps = kMxThreads / 32;
 
@@ -382,7 +384,7 @@ int admmq_mx_quantize(const void* x, int x_dtype, int64_t rows, int k, int64_t l
   int rc = device_ok();
   if (rc) return rc;
   const long long row_tiles = (rows + 127) / 128;
-  const bool small = row_tiles * cdiv(k, 512) < 2 * num_sms();
+  const bool small = row_tiles * cdiv(k, 512) < 4 * num_sms();
   const int spans = cdiv(k, small ? 128 : 512);
   const long long grid = row_tiles * spans;
   if (grid > 0x7FFFFFFFll) return ADMMQ_ERR_UNSUPPORTED;
@@ -409,7 +411,7 @@ int admmq_mx_dequantize(const uint8_t* codes, const uint8_t* scale, int64_t rows
   int rc = device_ok();
   if (rc) return rc;
   const long long row_tiles = (rows + 127) / 128;
-  const bool small = row_tiles * cdiv(k, 512) < 2 * num_sms();
+  const bool small = row_tiles * cdiv(k, 512) < 4 * num_sms();
   const int spans = cdiv(k, small ? 128 : 512);
   const long long grid = row_tiles * spans;
   if (grid > 0x7FFFFFFFll) return ADMMQ_ERR_UNSUPPORTED;
