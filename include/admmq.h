@@ -264,8 +264,8 @@ int admmq_pack(const uint8_t* codes_dev, int d_in, int d_out, int bits, uint32_t
  *              in [0, 2^bits - 1] (as the solve, the RTN start and GPTQ give them).
  *   out_dev    fp32, bf16 or fp16 (out_dtype) [m][d_out], contiguous, 16-byte
  *              aligned.
- * m >= 0 (nothing is launched for 0), at most 2^30.  Deterministic: no sum's
- * order depends on timing. */
+ * m >= 0 (nothing is launched for 0), at most 2^30.  out_dev overlaps no
+ * input.  Deterministic: no sum's order depends on timing. */
 int admmq_packed_matmul(const void* x_dev, int x_dtype, int64_t m, int64_t ldx,
                         const uint32_t* packed_dev, const float* scale_dev, const float* zero_dev,
                         int d_in, int d_out, int bits, int group, void* out_dev, int out_dtype,
@@ -290,7 +290,8 @@ int admmq_packed_matmul(const void* x_dev, int x_dtype, int64_t m, int64_t ldx,
  *          means 1.  Must be NULL for mxfp4.
  * k is a multiple of 32, at most 2^24; rows >= 0 (nothing is launched for 0),
  * at most 2^30.  codes, scale and the 16/32-bit matrices are 16-byte aligned,
- * their row distances (ld, in elements) multiples of 16 bytes. */
+ * their row distances (ld, in elements) multiples of 16 bytes; outputs overlap
+ * no input. */
 enum { ADMMQ_MX_MXFP4 = 0, ADMMQ_MX_NVFP4 = 1 };
 
 /* Bytes of the scale tiles of a [rows][k] matrix (0 for invalid sizes or no rows). */
