@@ -232,10 +232,10 @@ int launch_pair(const uint8_t* w_codes, const uint8_t* x_codes, const MxArgs& q,
 // `fits`: every stage of a block is resident at once.
 int plan_tile(MxArgs& p, int fmt, bool& fits) {
   const int nsf = kMxBK / mx_tile_k(fmt);
-  const int xt = (p.tn + 127) / 128, tiles = p.tiles_n * (p.tn < 128 ? 1 : cdiv(p.m, p.tn));
+  const int tiles = p.tiles_n;
   int ranks = 1;
   while (ranks < 8 && 2 * ranks <= p.kblocks && tiles * 2 * ranks <= cluster_ctas(2 * ranks)) ranks *= 2;
-  p.stage_bytes = 128 * 128 + ((p.tn * 128 + 1023) & ~1023) + (((1 + xt) * nsf * kScaleTile + 1023) & ~1023);
+  p.stage_bytes = 128 * 128 + ((p.tn * 128 + 1023) & ~1023) + ((2 * nsf * kScaleTile + 1023) & ~1023);
   p.part_bytes = ranks > 1 ? ranks * cdiv(p.tn, ranks) * 512 : 0;
   // everything that a block reads on its way at once, or half of an SM's
   // shared memory where the blocks are more than the SMs
@@ -258,8 +258,7 @@ int launch_tile(MxArgs& p, bool fused, cudaStream_t st) {
   constexpr int NSF = kMxBK / MxFormat<FMT>::TILE_K;
   bool fits;
   const int ranks = plan_tile(p, FMT, fits);
-  const int xt = (p.tn + 127) / 128, tiles = p.tiles_n * (p.tn < 128 ? 1 : cdiv(p.m, p.tn));
-  const int cols = ((p.tn + 31) & ~31) + 4 * NSF * (1 + xt);
+  const int tiles = p.tiles_n, cols = ((p.tn + 31) & ~31) + 8 * NSF;
   p.tmem_cols = 32;
   while (p.tmem_cols < cols) p.tmem_cols *= 2;
   const int smem = tmem_fair_smem(p.stages * p.stage_bytes + p.part_bytes + 1024 + 16 * p.stages + 64, p.tmem_cols);
@@ -317,7 +316,7 @@ MxArgs mx_args(const uint8_t* a_scale, const float* a_tensor_scale, const uint8_
   p.m = (int)m;
   p.n = n;
   p.k = k;
-  p.tn = m <= 128 ? ((int)m + 15) / 16 * 16 : 256;
+  p.tn = m <= 128 ? ((int)m + 15) / 16 * 16 : 0;  // (k_mx_pair has its own)
   p.tiles_n = cdiv(n, 128);
   p.kblocks = cdiv(k, kMxBK);
   p.col_tiles = cdiv(k, mx_tile_k(fmt));

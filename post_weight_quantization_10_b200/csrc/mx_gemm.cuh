@@ -80,7 +80,6 @@ struct MxArgs {
   void* out;
   int m, n, k;                 // tokens, output columns, reduction
   int tn;                      // tokens of a tile: a multiple of 16 up to 128 that holds all
-                               // of them, or 128 or 256 (tiles start at a scale tile's row 0)
   int tiles_n;                 // 128-column tiles
   int kblocks, col_tiles;      // 256-element stages; scale tiles along k
   int stages, stage_bytes, part_bytes;  // part_bytes: the ranks' partial tiles
@@ -163,7 +162,6 @@ __global__ void __launch_bounds__(kMxTileThreads)
   extern __shared__ uint8_t smem_raw[];
   // (an offset, not a cast: the compiler has to see shared memory behind it)
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
-  const int xt = (p.tn + 127) >> 7;  // 128-row scale tiles of the activations
   const int x_bytes = p.tn * 128;
   const int x_off = 128 * 128, sw_off = x_off + ((x_bytes + 1023) & ~1023),
             sx_off = sw_off + NSF * kScaleTile;
@@ -178,8 +176,7 @@ __global__ void __launch_bounds__(kMxTileThreads)
   uint32_t rank, ranks;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
   asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(ranks));
-  const long long tile = blockIdx.x / ranks;
-  const int tn_tile = (int)(tile % p.tiles_n), tm_tile = (int)(tile / p.tiles_n);
+  const int tn_tile = blockIdx.x / ranks;
   const int kb0 = (int)((long long)rank * p.kblocks / ranks);
   const int kb1 = (int)((long long)(rank + 1) * p.kblocks / ranks);
 
@@ -205,22 +202,17 @@ __global__ void __launch_bounds__(kMxTileThreads)
       bool ok = true;
       Ring r;
       int loads = 0;
-      // a token tile's 128-row scale tiles that exist
-      const int x_row = tm_tile * p.tn >> 7, xrows = FUSED ? 0 : min(xt, (p.m + 127) / 128 - x_row);
       const uint8_t* ws = p.w_scale + (long long)tn_tile * p.col_tiles * kScaleTile;
-      const uint8_t* xs = p.x_scale + (long long)x_row * p.col_tiles * kScaleTile;
       auto load_w = [&](int kb, uint32_t st, uint32_t bar) {
         const int sf = min(NSF, p.col_tiles - kb * NSF) * kScaleTile;  // scale bytes of this stage
-        mbar_arrive_expect_tx(bar, 128 * 128 + sf + (FUSED ? 0 : x_bytes + sf * xrows));
+        mbar_arrive_expect_tx(bar, 128 * 128 + sf + (FUSED ? 0 : x_bytes + sf));
         tma_load_2d(st, &p.w, kb * 128, tn_tile * 128, bar);
         bulk_load(st + sw_off, ws + kb * NSF * kScaleTile, sf, bar);
       };
       auto load_x = [&](int kb, uint32_t st, uint32_t bar) {
         const int sf = min(NSF, p.col_tiles - kb * NSF) * kScaleTile;
-        tma_load_2d(st + x_off, &p.x, kb * 128, tm_tile * p.tn, bar);
-        for (int i = 0; i < xrows; ++i)
-          bulk_load(st + sx_off + i * NSF * kScaleTile,
-                    xs + ((long long)i * p.col_tiles + kb * NSF) * kScaleTile, sf, bar);
+        tma_load_2d(st + x_off, &p.x, kb * 128, 0, bar);
+        bulk_load(st + sx_off, p.x_scale + (long long)kb * NSF * kScaleTile, sf, bar);
       };
       // the weights of every stage before the first activation, which the
       // kernel in front may still be writing
@@ -266,9 +258,7 @@ __global__ void __launch_bounds__(kMxTileThreads)
         for (int i = 0; i < NSF; ++i) {
           if (i < tiles) {
             tmem_copy_scales(sfw + 4 * i, dsw0 + at + i * (kScaleTile >> 4));
-            tmem_copy_scales(sfx + 4 * i * xt, dsx0 + at + i * (kScaleTile >> 4));
-            if (xt > 1)
-              tmem_copy_scales(sfx + 4 * (i * xt + 1), dsx0 + at + (NSF + i) * (kScaleTile >> 4));
+            tmem_copy_scales(sfx + 4 * i, dsx0 + at + i * (kScaleTile >> 4));
           }
         }
 #pragma unroll
@@ -277,7 +267,7 @@ __global__ void __launch_bounds__(kMxTileThreads)
             const int t = FMT == MX_MXFP4 ? j >> 1 : j;
             const uint32_t sf = FMT == MX_MXFP4 ? 2u * (j & 1) : 0u;
             mma_mx<FMT>(tmem, dw0 + at + 2 * j, dx0 + at + 2 * j, idesc_mx<FMT>(128, p.tn, sf),
-                        sfw + 4 * t, sfx + 4 * t * xt, (kb > kb0 || j > 0) ? 1u : 0u);
+                        sfw + 4 * t, sfx + 4 * t, (kb > kb0 || j > 0) ? 1u : 0u);
           }
         }
         mma_commit(smem_u32(&empty[r.i]));
@@ -292,9 +282,9 @@ __global__ void __launch_bounds__(kMxTileThreads)
   const uint32_t ta = tmem + ((uint32_t)((warp & 3) * 32) << 16);
   bool ok = true;
   const long long col = (long long)tn_tile * 128 + row;
-  const int tokens = min(p.tn, p.m - tm_tile * p.tn);
+  const int tokens = p.m;
   const float2 g = output_factors(p.gw, p.gx);
-  T* out = reinterpret_cast<T*>(p.out) + (long long)tm_tile * p.tn * p.n + col;
+  T* out = reinterpret_cast<T*>(p.out) + col;
   const int per = (tokens + (int)ranks - 1) / (int)ranks;  // tokens that a rank sums
   const uint32_t part = smem_u32(smem) + p.stages * p.stage_bytes;  // [ranks][per][128]
   if (FUSED && warp >= 2) {
