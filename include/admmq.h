@@ -271,6 +271,22 @@ int admmq_packed_matmul(const void* x_dev, int x_dtype, int64_t m, int64_t ldx,
                         int d_in, int d_out, int bits, int group, void* out_dev, int out_dtype,
                         void* stream);
 
+/* Test hook: how admmq_packed_matmul lays out m tokens on a device of `sms`
+ * SMs (0: the current device's); nothing is launched and no pointer is needed.
+ *   plan[0]  tokens of a tile (8 or 16: few tokens; 64, 128 or 512: many)
+ *   plan[1]  weight rows of a tile
+ *   plan[2]  tiles (few tokens: blocks of weight rows)
+ *   plan[3]  of them, how many are begun at once (each is a cluster's)
+ *   plan[4]  CTAs of a cluster; with 512 tokens a CTA has half of the tokens,
+ *            else plan[5] of the row's 128-column chunks, from plan[5] x rank on
+ *   plan[6]  few tokens: chunks of a pipeline stage; many: operand stages
+ *   plan[7]  few tokens: groups of a stage; many: buffers of packed chunks
+ *   plan[8]  few tokens: 1 if the activations are staged with the weights
+ *   plan[9]  few tokens: 1 if scales and zero points move in 16-byte pieces
+ *            (their pointers permitting) */
+int admmq_debug_packed_plan(int64_t m, int d_in, int d_out, int bits, int group, int sms,
+                            int plan[10]);
+
 /* ------------------------------------------- microscaled 4-bit floating point --
  * Matrices of e2m1 elements (0, 1/2, 1, 3/2, 2, 3, 4, 6 and their negatives)
  * with one 8-bit scale per block of a row, the tensor cores' own formats:

@@ -129,6 +129,7 @@ def lib():
                             _sz, _vp]),
         "admmq_packed_matmul": (_i, [_vp, _i, _i64, _i64, _vp, _vp, _vp, _i, _i, _i, _i, _vp, _i,
                                      _vp]),
+        "admmq_debug_packed_plan": (_i, [_i64, _i, _i, _i, _i, _i, _vp]),
         "admmq_mx_scale_bytes": (_sz, [_i64, _i, _i]),
         "admmq_mx_quantize": (_i, [_vp, _i, _i64, _i, _i64, _i, _vp, _vp, _vp, _vp]),
         "admmq_mx_dequantize": (_i, [_vp, _vp, _i64, _i, _i, _vp, _vp, _i, _i64, _vp]),
@@ -428,6 +429,15 @@ def packed_matmul(x: torch.Tensor, packed: torch.Tensor, scale: torch.Tensor, ze
             _row_stride(x), packed.data_ptr(), scale.data_ptr(), zero.data_ptr(), d, n, bits,
             d // groups, out.data_ptr(), DTYPES[dtype])
     return out
+
+
+def debug_packed_plan(m: int, d_in: int, d_out: int, bits: int, group: int, sms: int = 0) -> dict:
+    """How packed_matmul lays out a call (test hook, see include/admmq.h)."""
+    plan = (ctypes.c_int * 10)()
+    _check(lib().admmq_debug_packed_plan(m, d_in, d_out, bits, group, sms, plan),
+           "admmq_debug_packed_plan")
+    return dict(zip(("tokens", "rows", "tiles", "at_once", "ranks", "range", "stage", "groups",
+                     "staged", "vec_scales"), plan))
 
 
 # ------------------------------------------- microscaled 4-bit floating point

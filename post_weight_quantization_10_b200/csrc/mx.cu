@@ -234,7 +234,7 @@ int plan_tile(MxArgs& p, int fmt, bool& fits) {
   const int nsf = kMxBK / mx_tile_k(fmt);
   const int tiles = p.tiles_n;
   int ranks = 1;
-  while (ranks < 8 && 2 * ranks <= p.kblocks && tiles * 2 * ranks <= cluster_ctas(2 * ranks)) ranks *= 2;
+  while (ranks < 8 && 2 * ranks <= p.kblocks && tiles * 2 * ranks <= cluster_ctas(2 * ranks, num_sms())) ranks *= 2;
   p.stage_bytes = 128 * 128 + ((p.tn * 128 + 1023) & ~1023) + ((2 * nsf * kScaleTile + 1023) & ~1023);
   p.part_bytes = ranks > 1 ? ranks * cdiv(p.tn, ranks) * 512 : 0;
   // everything that a block reads on its way at once, or half of an SM's

@@ -66,6 +66,7 @@ struct FewPlan {
   int blocks;                      // row blocks
   int rank_shift, passes, groups;  // log2 ranks; groups of a span; of a stage
   int x_staged;
+  int vec_scales;                  // every stage's scales begin and end on whole 16-byte pieces
   int pitch, x_pitch;              // of a row in words, of a token in bytes
   int s_off, bytes;                // of a stage
   int x_off, x_bytes, smem;
@@ -108,8 +109,8 @@ __global__ void __launch_bounds__(kFewThreads, few_blocks(RT))
   const int r = lane >> 2, q = lane & 3, rt = RT == 1 ? 0 : warp & (RT - 1), kw = warp / RT;
   const int passes = st.passes;
   const bool vec = (p.words & 3) == 0;  // rows of words start on 16 bytes
-  const bool vec_s = ((p.groups | st.groups) & 3) == 0 &&
-                     (((uintptr_t)p.scale | (uintptr_t)p.zero) & 15) == 0;  // so do their scales
+  const bool vec_s = st.vec_scales &&
+                     (((uintptr_t)p.scale | (uintptr_t)p.zero) & 15) == 0;  // so do a stage's scales
 
   // Words, scales and zero points of the spans from sp on into a stage.  The
   // words of a row are one bulk copy (rows that start on 16 bytes; others go

@@ -38,26 +38,42 @@ inline bool make_w_map(CUtensorMap* m, const PackedArgs& p, int box_rows) {
 }
 
 // Ranks that share the reduction of a tile, where the tiles are too few.
-inline int split_ranks(long long tiles, int chunks) {
+inline int split_ranks(long long tiles, int chunks, int sms) {
   int ranks = 1;
-  while (ranks < 8 && chunks >= 4 * ranks && 2 * ranks * tiles <= cluster_ctas(2 * ranks)) ranks *= 2;
+  while (ranks < 8 && chunks >= 4 * ranks && 2 * ranks * tiles <= cluster_ctas(2 * ranks, sms)) ranks *= 2;
   return ranks;
 }
 
 // About how long a tile shape takes: rounds of tiles x chunks of a rank x a
 // chunk's time, plus what adding partial tiles takes.
-inline double tile_time(const PackedArgs& p, int tokens, int ctas, double chunk_us) {
+inline double tile_time(const PackedArgs& p, int tokens, int ctas, double chunk_us, int sms) {
   const int chunks = cdiv(p.k, 128);
   const long long tiles = (long long)cdiv(p.m, tokens) * cdiv(p.n, 128);
-  const int ranks = ctas == 1 ? split_ranks(tiles, chunks) : 1;
-  const int at_once = ranks > 1 ? cluster_ctas(ranks) / ranks : num_sms() / ctas;
+  const int ranks = ctas == 1 ? split_ranks(tiles, chunks, sms) : 1;
+  const int at_once = ranks > 1 ? cluster_ctas(ranks, sms) / ranks : sms / ctas;
   return (double)((tiles + at_once - 1) / at_once) * cdiv(chunks, ranks) * chunk_us + (ranks > 1 ? 3.0 : 0.0);
 }
 
-template <typename X, int TN, int C, bool BY_BITS>
-int launch_gemm(const PackedArgs& p, cudaStream_t st) {
-  using Cfg = PackedCfg<TN, C>;
+// The tile shape that is estimated to take least: tokens of a tile, 64, 128 or
+// 512 (two CTAs).  A chunk's times are measured (33 tokens of 4096 -> 24576: 47 us
+// in two rounds of 32 chunks; 256: 96 us in three; 4096: 890 us in 21): 64 tokens
+// cost as much as the decoding that they share, 512 a cluster's MMAs.
+inline int packed_tile(const PackedArgs& p, int sms) {
+  const double t64 = tile_time(p, 64, 1, 0.74, sms), t128 = tile_time(p, 128, 1, 1.0, sms),
+               t512 = tile_time(p, 512, 2, 1.32, sms);
+  return t64 <= t128 && t64 <= t512 ? 64 : t128 <= t512 ? 128 : 512;
+}
+
+// How a call is laid out (all but the tensor maps of `a`).
+struct PackedGemmPlan {
   PackedGemmArgs a;
+  int ranks, clusters, smem;
+};
+
+template <int TN, int C>
+int plan_gemm(const PackedArgs& p, int sms, PackedGemmPlan& plan) {
+  using Cfg = PackedCfg<TN, C>;
+  PackedGemmArgs& a = plan.a;
   a.p = p;
   a.tiles_m = cdiv(p.m, TN * C);
   const long long tiles = (long long)a.tiles_m * cdiv(p.n, 128);
@@ -66,7 +82,7 @@ int launch_gemm(const PackedArgs& p, cudaStream_t st) {
   a.chunks = cdiv(p.k, 128);
   a.passes = 128 / p.group;
   a.w_tma = p.words % 4 == 0;
-  int ranks = C == 1 ? split_ranks(tiles, a.chunks) : C;
+  int ranks = C == 1 ? split_ranks(tiles, a.chunks, sms) : C;
   // Shared memory: the ranks' partial tiles; packed chunks, which come from HBM,
   // a long way off (a third of the rings, at most 16); operand stages the rest.
   // A decoder group may wait for a buffer that others have yet to use once:
@@ -88,10 +104,22 @@ int launch_gemm(const PackedArgs& p, cudaStream_t st) {
     if (ranks == C) return ADMMQ_ERR_UNSUPPORTED;
   }
   a.range = C == 1 ? cdiv(a.chunks, ranks) : a.chunks;
+  plan.smem = tmem_fair_smem(a.stages * Cfg::STAGE + a.wbufs * wbytes + a.part_bytes + 2048, Cfg::TMEM_COLS);
+  const int most = C == 1 && ranks > 1 ? a.tiles : sms / ranks;
+  plan.ranks = ranks;
+  plan.clusters = a.tiles < most ? a.tiles : most;
+  return ADMMQ_OK;
+}
+
+template <typename X, int TN, int C, bool BY_BITS>
+int launch_gemm(const PackedArgs& p, int sms, cudaStream_t st) {
+  using Cfg = PackedCfg<TN, C>;
+  PackedGemmPlan plan;
+  int rc = plan_gemm<TN, C>(p, sms, plan);
+  if (rc) return rc;
+  PackedGemmArgs& a = plan.a;
   if (!make_x_map(&a.x, p, __is_same(X, __nv_bfloat16), TN)) return ADMMQ_ERR_CUDA;
   if (a.w_tma && !make_w_map(&a.w, p, Cfg::ROWS)) return ADMMQ_ERR_CUDA;
-  int smem = a.stages * Cfg::STAGE + a.wbufs * wbytes + a.part_bytes + 2048;
-  smem = tmem_fair_smem(smem, Cfg::TMEM_COLS);
   const void* kern;
   if constexpr (BY_BITS) {
     static const void* const table[8] = {
@@ -103,17 +131,15 @@ int launch_gemm(const PackedArgs& p, cudaStream_t st) {
   } else {
     kern = (const void*)k_packed_gemm<X, TN, C, 0>;
   }
-  CK(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
-  const int most = C == 1 && ranks > 1 ? a.tiles : num_sms() / ranks;
-  const int clusters = a.tiles < most ? a.tiles : most;
+  CK(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, plan.smem));
   cudaLaunchConfig_t lc = {};
-  lc.gridDim = dim3((unsigned)(clusters * ranks));
+  lc.gridDim = dim3((unsigned)(plan.clusters * plan.ranks));
   lc.blockDim = dim3(Cfg::THREADS);
-  lc.dynamicSmemBytes = smem;
+  lc.dynamicSmemBytes = plan.smem;
   lc.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = ranks;
+  attr[0].val.clusterDim.x = plan.ranks;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   lc.attrs = attr;
@@ -124,17 +150,14 @@ int launch_gemm(const PackedArgs& p, cudaStream_t st) {
   return ADMMQ_OK;
 }
 
-// The tile shape that is estimated to take least.  A chunk's times are measured
-// (33 tokens of 4096 -> 24576: 47 us in two rounds of 32 chunks; 256: 96 us in
-// three; 4096: 890 us in 21): 64 tokens cost as much as the decoding that they
-// share, 512 a cluster's MMAs.
 template <typename X>
 int packed_gemm(const PackedArgs& p, cudaStream_t st) {
-  const double t64 = tile_time(p, 64, 1, 0.74), t128 = tile_time(p, 128, 1, 1.0),
-               t512 = tile_time(p, 512, 2, 1.32);
-  if (t64 <= t128 && t64 <= t512) return launch_gemm<X, 64, 1, true>(p, st);
-  if (t128 <= t512) return launch_gemm<X, 128, 1, true>(p, st);
-  return launch_gemm<X, 256, 2, false>(p, st);
+  const int sms = num_sms();
+  switch (packed_tile(p, sms)) {
+    case 64: return launch_gemm<X, 64, 1, true>(p, sms, st);
+    case 128: return launch_gemm<X, 128, 1, true>(p, sms, st);
+    default: return launch_gemm<X, 256, 2, false>(p, sms, st);
+  }
 }
 
 }  // namespace admmq

@@ -9,7 +9,7 @@ namespace admmq {
 // not straddle the GPU's processing clusters, whose sizes leave some SMs over:
 // 48 clusters of three (144 CTAs) took two rounds where 48 pairs took one, and
 // 32 clusters of four are the most that run together.
-inline int cluster_ctas(int size) { return size <= 2 ? num_sms() / size * size : 128; }
+inline int cluster_ctas(int size, int sms) { return size <= 2 ? sms / size * size : 128; }
 
 // Shared memory to ask for, so that blocks which fit an SM together never ask
 // for more than its 512 tensor-memory columns: the CTAs of a cluster wait for
