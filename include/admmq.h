@@ -264,7 +264,7 @@ int admmq_pack(const uint8_t* codes_dev, int d_in, int d_out, int bits, uint32_t
  *              in [0, 2^bits - 1] (as the solve, the RTN start and GPTQ give them).
  *   out_dev    fp32, bf16 or fp16 (out_dtype) [m][d_out], contiguous, 16-byte
  *              aligned.
- * m >= 0 (nothing is launched for 0), at most 2^30.  out_dev overlaps no
+ * m >= 0 (nothing is launched for 0) and d_in at most 2^30.  out_dev overlaps no
  * input.  Deterministic: no sum's order depends on timing. */
 int admmq_packed_matmul(const void* x_dev, int x_dtype, int64_t m, int64_t ldx,
                         const uint32_t* packed_dev, const float* scale_dev, const float* zero_dev,

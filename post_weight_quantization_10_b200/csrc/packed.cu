@@ -42,7 +42,7 @@ FewLaunch plan_few(const PackedArgs& p, int sms) {
   // all activations next to two stages in half of the shared memory? (8 tokens of
   // 4096 -> 24576 at 3 bits: 28.9 us against 31.6 staged, 6 tokens 24.5 / 31.0; 2 of
   // 12288 -> 4096 13.3 / 12.6)
-  const bool one = p.m <= 8 && (long long)p.m * (spans * 256 + 64) <= 70 * 1024;
+  const bool one = p.m <= 8 && p.m * (spans * 256ll + 64) <= 70 * 1024;
   const int rows = one ? 16 : 64, blocks = cdiv(p.n, rows);
   // ranks, as long as all blocks run at once, three on an SM (a fourth block's
   // worth: 4 tokens of 12288 -> 4096 20.9 us instead of 14.6)
@@ -94,9 +94,11 @@ int launch_few(PackedArgs p, cudaStream_t st) {
   return ADMMQ_OK;
 }
 
-// Sizes that the product takes.
+// Sizes that the product takes.  (Rows up to 2^30 columns: the kernels count
+// columns, also those of a stage or two past the last, in 32 bits.)
 bool packed_shape_ok(int64_t m, int d_in, int d_out, int bits, int group) {
-  return m >= 0 && m <= (1ll << 30) && d_in > 0 && d_out > 0 && d_in % 32 == 0 &&
+  return m >= 0 && m <= (1ll << 30) && d_in > 0 && d_in <= (1 << 30) && d_out > 0 &&
+         d_in % 32 == 0 &&
          (group == 32 || group == 64 || group == 128) && d_in % group == 0 && bits >= 1 && bits <= 8;
 }
 

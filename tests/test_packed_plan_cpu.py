@@ -1,5 +1,7 @@
 """How the packed product lays a call out, checked on the host: every copy of
 the few-token kernel has to start on its size and to stay inside its row."""
+import ctypes
+
 import pytest
 
 SMS = 148
@@ -56,3 +58,17 @@ def test_every_column_has_one_rank(A):
                 assert plan["ranks"] * plan["range"] * 128 >= k
                 assert plan["groups"] == plan["stage"] * 4
                 assert plan["tiles"] * plan["rows"] >= n
+
+
+def test_the_longest_rows(A):
+    """Rows up to 2^30 columns: their activations do not fit the shared memory,
+    every position is a 32-bit number.  Longer ones are refused."""
+    for m in (1, 8, 12):
+        plan = A.debug_packed_plan(m, 1 << 30, 16, 1, 32, SMS)
+        assert plan["staged"] == 1 and plan["ranks"] * plan["range"] * 128 >= 1 << 30
+    assert A.debug_packed_plan(13, 1 << 30, 16, 1, 32, SMS)["range"] * 8 * 128 == 1 << 30
+    p = [ctypes.c_void_p(0x10000 * (i + 1)) for i in range(5)]
+    for k in ((1 << 30) + 32, (1 << 31) - 64):
+        for m in (1, 40):
+            assert A.lib().admmq_packed_matmul(p[0], 1, m, k, p[1], p[2], p[3], k, 16, 1, 32, p[4],
+                                               1, None) == A.ERR_INVALID_ARG
