@@ -39,9 +39,13 @@ inline PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
+// Whether the current device is one of those that the library is built for.  Its
+// context becomes the calling thread's (cudaSetDevice does that, cudaGetDevice
+// does not): a thread whose first use of the GPU is a call of this library
+// could not encode a tensor map without one.
 inline int device_ok() {
   int dev = 0, major = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return ADMMQ_ERR_CUDA;
+  if (cudaGetDevice(&dev) != cudaSuccess || cudaSetDevice(dev) != cudaSuccess) return ADMMQ_ERR_CUDA;
   if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess)
     return ADMMQ_ERR_CUDA;
   return major == 10 ? ADMMQ_OK : ADMMQ_ERR_UNSUPPORTED;
