@@ -51,6 +51,12 @@ inline int device_ok() {
   return major == 10 ? ADMMQ_OK : ADMMQ_ERR_UNSUPPORTED;
 }
 
+// Shared memory that a block may ask for at launch beyond its static variables.
+// Kernels whose plans differ from call to call are allowed the most that any
+// plan asks for, not their own: the limit belongs to the kernel, and another
+// thread could set its own between this thread's setting and launch.
+constexpr int kMaxSmem = 227 * 1024;
+
 inline int cdiv(long long a, long long b) { return (int)((a + b - 1) / b); }
 
 }  // namespace admmq

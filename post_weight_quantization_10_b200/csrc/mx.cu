@@ -263,7 +263,7 @@ int launch_tile(MxArgs& p, bool fused, cudaStream_t st) {
   while (p.tmem_cols < cols) p.tmem_cols *= 2;
   const int smem = tmem_fair_smem(p.stages * p.stage_bytes + p.part_bytes + 1024 + 16 * p.stages + 64, p.tmem_cols);
   auto kern = fused ? k_mx_tile<FMT, T, true> : k_mx_tile<FMT, T, false>;
-  CK(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+  CK(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem));
   cudaLaunchConfig_t lc = {};
   lc.gridDim = dim3((unsigned)(tiles * ranks));
   lc.blockDim = dim3(kMxTileThreads);

@@ -30,6 +30,10 @@ const void* few_kernel(int bits) {
   return table[bits - 1];
 }
 
+// Shared memory of a block at most: half of an SM's, or a third (one stage of one
+// span takes less than either).
+constexpr int few_smem(bool one) { return (one ? 110 : 72) * 1024; }
+
 // How a call is laid out.
 struct FewLaunch {
   FewPlan plan;
@@ -53,7 +57,7 @@ FewLaunch plan_few(const PackedArgs& p, int sms) {
   int per = 1;
   while (per < most && per < range) per *= 2;
   FewPlan plan(rows, per, range, p.bits, p.group, p.m, !one);
-  while (plan.smem > (one ? 110 : 72) * 1024 && per > 1) {
+  while (plan.smem > few_smem(one) && per > 1) {
     per /= 2;
     plan = FewPlan(rows, per, range, p.bits, p.group, p.m, !one);
   }
@@ -75,7 +79,7 @@ int launch_few(PackedArgs p, cudaStream_t st) {
   const void* kern = l.one       ? few_kernel<X, 1, 1>(p.bits)
                      : p.m <= 8  ? few_kernel<X, 1, 4>(p.bits)
                                  : few_kernel<X, 2, 4>(p.bits);
-  CK(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, l.plan.smem));
+  CK(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, few_smem(l.one)));
   cudaLaunchConfig_t lc = {};
   lc.gridDim = dim3((unsigned)(l.grid * l.ranks));
   lc.blockDim = dim3(kFewThreads);

@@ -131,7 +131,7 @@ int launch_gemm(const PackedArgs& p, int sms, cudaStream_t st) {
   } else {
     kern = (const void*)k_packed_gemm<X, TN, C, 0>;
   }
-  CK(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, plan.smem));
+  CK(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem));
   cudaLaunchConfig_t lc = {};
   lc.gridDim = dim3((unsigned)(plan.clusters * plan.ranks));
   lc.blockDim = dim3(Cfg::THREADS);
