@@ -163,29 +163,25 @@ int dtype_size(int dtype) { return dtype == ADMMQ_DTYPE_F32 ? 4 : 2; }
 // Codes [rows][k / 2] in boxes of 128 bytes x box_rows, 128-byte swizzle,
 // bytes out of range read as zero (the code of 0).
 bool make_codes_map(CUtensorMap* m, const void* ptr, int k, int64_t rows, int box_rows) {
-  auto fn = encode_fn();
-  if (!fn) return false;
   cuuint64_t dims[2] = {(cuuint64_t)k / 2, (cuuint64_t)rows};
   cuuint64_t strides[1] = {(cuuint64_t)k / 2};
   cuuint32_t box[2] = {128, (cuuint32_t)box_rows};
   cuuint32_t estr[2] = {1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(ptr), dims, strides, box, estr,
+  return encode_tiled(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(ptr), dims, strides, box, estr,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
 // Scale tiles as rows of 128 words, boxes of `tiles` rows; rows out of range
 // read as zero.
 bool make_scales_map(CUtensorMap* m, const void* ptr, int64_t tiles, int box_rows) {
-  auto fn = encode_fn();
-  if (!fn) return false;
   cuuint64_t dims[2] = {kScaleTile / 4, (cuuint64_t)tiles};
   cuuint64_t strides[1] = {kScaleTile};
   cuuint32_t box[2] = {kScaleTile / 4, (cuuint32_t)box_rows};
   cuuint32_t estr[2] = {1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<void*>(ptr), dims, strides, box, estr,
+  return encode_tiled(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<void*>(ptr), dims, strides, box, estr,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
 template <int FMT, typename T>
@@ -232,14 +228,14 @@ int launch_pair(const uint8_t* w_codes, const uint8_t* x_codes, const MxArgs& q,
 // `fits`: every stage of a block is resident at once.
 int plan_tile(MxArgs& p, int fmt, bool& fits) {
   const int nsf = kMxBK / mx_tile_k(fmt);
-  const int tiles = p.tiles_n;
+  const int tiles = p.tiles_n, sms = num_sms();
   int ranks = 1;
-  while (ranks < 8 && 2 * ranks <= p.kblocks && tiles * 2 * ranks <= cluster_ctas(2 * ranks, num_sms())) ranks *= 2;
+  while (ranks < 8 && 2 * ranks <= p.kblocks && tiles * 2 * ranks <= cluster_ctas(2 * ranks, sms)) ranks *= 2;
   p.stage_bytes = 128 * 128 + ((p.tn * 128 + 1023) & ~1023) + ((2 * nsf * kScaleTile + 1023) & ~1023);
   p.part_bytes = ranks > 1 ? ranks * cdiv(p.tn, ranks) * 512 : 0;
   // everything that a block reads on its way at once, or half of an SM's
   // shared memory where the blocks are more than the SMs
-  const int blocks = cdiv(p.kblocks, ranks), room = tiles * ranks > num_sms() ? 108 * 1024 : 216 * 1024;
+  const int blocks = cdiv(p.kblocks, ranks), room = tiles * ranks > sms ? 108 * 1024 : 216 * 1024;
   p.stages = (room - p.part_bytes) / p.stage_bytes;
   fits = p.stages >= blocks;
   if (fits) p.stages = blocks;

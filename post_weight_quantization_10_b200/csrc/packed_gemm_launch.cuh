@@ -8,22 +8,18 @@
 namespace admmq {
 
 inline bool make_x_map(CUtensorMap* m, const PackedArgs& p, bool bf16, int box_rows) {
-  auto fn = encode_fn();
-  if (!fn) return false;
   cuuint64_t dims[2] = {(cuuint64_t)p.k, (cuuint64_t)p.m};
   cuuint64_t strides[1] = {(cuuint64_t)p.ldx * 2};
   cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
   cuuint32_t estr[2] = {1, 1};
-  return fn(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
+  return encode_tiled(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
             const_cast<void*>(p.x), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
 // Packed rows as bytes, boxes of a 128-code chunk (16 b bytes).
 inline bool make_w_map(CUtensorMap* m, const PackedArgs& p, int box_rows) {
-  auto fn = encode_fn();
-  if (!fn) return false;
   cuuint64_t dims[2] = {(cuuint64_t)p.words * 4, (cuuint64_t)p.n};
   cuuint64_t strides[1] = {(cuuint64_t)p.words * 4};
   cuuint32_t box[2] = {(cuuint32_t)(16 * p.bits), (cuuint32_t)box_rows};
@@ -32,9 +28,9 @@ inline bool make_w_map(CUtensorMap* m, const PackedArgs& p, int box_rows) {
                                 : p.bits == 4 ? CU_TENSOR_MAP_SWIZZLE_64B
                                 : p.bits == 8 ? CU_TENSOR_MAP_SWIZZLE_128B
                                               : CU_TENSOR_MAP_SWIZZLE_NONE;
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint32_t*>(p.packed), dims, strides,
+  return encode_tiled(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint32_t*>(p.packed), dims, strides,
             box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
 // Ranks that share the reduction of a tile, where the tiles are too few.
