@@ -355,6 +355,21 @@ int admmq_mx_linear(const void* x_dev, int x_dtype, int64_t m, int64_t ldx,
                     int fmt, void* out_dev, int out_dtype, void* ws_dev, size_t ws_bytes,
                     void* stream);
 
+/* The operators above (packed and mx products) have no context whose status
+ * word could say that a kernel's bounded pipeline wait gave up (about a second
+ * of SM clock cycles, which a GPU shared by time slices can pass as well): such
+ * a call returned ADMMQ_OK when it was launched, and the outputs that it could
+ * not compute are NaN.  This call waits for the stream and returns
+ * ADMMQ_ERR_TIMEOUT if that happened in any of these operators on the current
+ * device, in whatever stream, since the last check, and clears the record.  Not
+ * for a stream that is being captured. */
+int admmq_operators_check(void* stream);
+
+/* Test hook for it: a kernel on `stream` whose wait runs out, in translation
+ * unit 0 (mx), 1 (packed, few tokens), 2 or 3 (packed, many, bf16 or fp16
+ * activations).  It takes about a second; no fault or endless loop is involved. */
+int admmq_debug_give_up(int unit, void* stream);
+
 /* ------------------------------------------------------------ inspection --
  * Device buffers inside the workspace, for tests and diagnostics.
  * Operand encoding of the eigenbasis GEMMs (fp32-accurate split precision,

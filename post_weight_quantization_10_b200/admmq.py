@@ -129,6 +129,8 @@ def lib():
                             _sz, _vp]),
         "admmq_packed_matmul": (_i, [_vp, _i, _i64, _i64, _vp, _vp, _vp, _i, _i, _i, _i, _vp, _i,
                                      _vp]),
+        "admmq_operators_check": (_i, [_vp]),
+        "admmq_debug_give_up": (_i, [_i, _vp]),
         "admmq_debug_packed_plan": (_i, [_i64, _i, _i, _i, _i, _i, _vp]),
         "admmq_mx_scale_bytes": (_sz, [_i64, _i, _i]),
         "admmq_mx_quantize": (_i, [_vp, _i, _i64, _i, _i64, _i, _vp, _vp, _vp, _vp]),
@@ -583,6 +585,21 @@ def mx_linear(x: torch.Tensor, w: MxTensor, dtype: torch.dtype | None = None,
             _ptr_or_null(tensor_scale), *w._ptrs(), n, k, f, out.data_ptr(), DTYPES[dtype],
             _ptr_or_null(ws), need)
     return out
+
+
+def operators_check(device=None, stream=None):
+    """Wait for the stream and raise AdmmqError (ERR_TIMEOUT) if a kernel of the
+    packed or mx operators gave up a bounded wait on `device` since the last
+    check: the outputs that it could not compute are NaN."""
+    index = None if device is None else torch.device(device).index
+    if index is None:
+        index = torch.cuda.current_device()
+    _launch("admmq_operators_check", torch.device("cuda", index), stream)
+
+
+def debug_give_up(unit: int, stream=None):
+    """Failure-path test hook (see include/admmq.h)."""
+    _check(lib().admmq_debug_give_up(unit, _stream(stream)), "admmq_debug_give_up")
 
 
 def project(wtilde, V, sigma, rsig, hdiag, bits, group, grid, codes, scale, zero, P_hi, P_lo,

@@ -18,7 +18,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libadmmq.so")
 SOURCES = ["admmq.cu", "mx.cu", "packed.cu", "packed_gemm_bf16.cu", "packed_gemm_fp16.cu"]
-HEADERS = ["host.cuh", "async.cuh", "ptx.cuh", "gemm.cuh", "kernels.cuh", "admm_loop.cuh", "gptq.cuh", "mx.cuh",
+HEADERS = ["host.cuh", "async.cuh", "gave_up.cuh", "ptx.cuh", "gemm.cuh", "kernels.cuh", "admm_loop.cuh", "gptq.cuh", "mx.cuh",
            "mx_gemm.cuh", "packed.cuh", "packed_few.cuh", "packed_gemm.cuh",
            "packed_gemm_launch.cuh", "tmem_fair.cuh"]
 INCLUDE = os.path.join(os.path.dirname(HERE), "include", "admmq.h")

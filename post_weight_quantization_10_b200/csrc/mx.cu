@@ -6,6 +6,10 @@
 #include "mx_gemm.cuh"
 #include "tmem_fair.cuh"
 
+namespace admmq {
+extern const GaveUp mx_gave_up = {take_gave_up, launch_give_up};
+}
+
 using namespace admmq;
 
 namespace {

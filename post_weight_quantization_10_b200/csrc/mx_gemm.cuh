@@ -8,6 +8,7 @@
 #pragma once
 #include "async.cuh"
 #include "../../include/admmq.h"
+#include "gave_up.cuh"
 #include "mx.cuh"
 #include "ptx.cuh"
 
@@ -343,6 +344,7 @@ __global__ void __launch_bounds__(kMxTileThreads)
     }
   }
   __syncthreads();
+  report_gave_up(*abort_flag);
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, p.tmem_cols);
@@ -576,6 +578,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxPairThreads, 1)
     }
   }
   __syncthreads();
+  report_gave_up(*abort_flag);
   cluster_sync();
   if (warp == 1) {
     tc_fence_after();

@@ -9,6 +9,7 @@ using namespace admmq;
 namespace admmq {
 int packed_gemm_bf16(const PackedArgs& p, cudaStream_t st);  // packed_gemm_bf16.cu
 int packed_gemm_fp16(const PackedArgs& p, cudaStream_t st);  // packed_gemm_fp16.cu
+extern const GaveUp mx_gave_up, packed_bf16_gave_up, packed_fp16_gave_up;  // mx.cu and these
 }  // namespace admmq
 
 namespace {
@@ -168,4 +169,24 @@ extern "C" int admmq_debug_packed_plan(int64_t m, int d_in, int d_out, int bits,
   const int v[10] = {tile, 128, g.a.tiles, g.clusters, g.ranks, g.a.range, g.a.stages, g.a.wbufs, 0, 0};
   for (int i = 0; i < 10; ++i) plan[i] = v[i];
   return ADMMQ_OK;
+}
+
+// The words of all units with operator kernels: mx, few tokens, many in bf16 and in fp16.
+static const GaveUp* gave_up_unit(int i) {
+  static const GaveUp few = {take_gave_up, launch_give_up};
+  const GaveUp* const units[] = {&mx_gave_up, &few, &packed_bf16_gave_up, &packed_fp16_gave_up};
+  return i >= 0 && i < 4 ? units[i] : nullptr;
+}
+
+extern "C" int admmq_operators_check(void* stream) {
+  int rc = device_ok(), any = 0;
+  for (int i = 0; rc == ADMMQ_OK && gave_up_unit(i); ++i)
+    rc = gave_up_unit(i)->take(&any, (cudaStream_t)stream);
+  return rc ? rc : any ? ADMMQ_ERR_TIMEOUT : ADMMQ_OK;
+}
+
+extern "C" int admmq_debug_give_up(int unit, void* stream) {
+  if (!gave_up_unit(unit)) return ADMMQ_ERR_INVALID_ARG;
+  const int rc = device_ok();
+  return rc ? rc : gave_up_unit(unit)->give_up((cudaStream_t)stream);
 }

@@ -16,6 +16,7 @@
 // groups' activations set to zero.
 #pragma once
 #include "async.cuh"
+#include "gave_up.cuh"
 #include "packed.cuh"
 #include "ptx.cuh"
 
@@ -374,6 +375,8 @@ __global__ void __launch_bounds__(kFewThreads, few_blocks(RT))
     }
     if (ranks > 1) cluster_sync();  // the sums stay until every rank has read them
   }
+  __syncthreads();
+  report_gave_up(abort_flag);
   if (!ok) {  // copies in flight land before the block retires (about 1 ms)
     const long long t0 = clock64();
     while (clock64() - t0 < 2000000LL) {

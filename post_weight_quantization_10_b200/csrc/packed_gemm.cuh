@@ -20,6 +20,7 @@
 // with a converged MMA warp, 0.91 with the decoding shared by two CTAs.
 #pragma once
 #include "async.cuh"
+#include "gave_up.cuh"
 #include "packed.cuh"
 #include "ptx.cuh"
 
@@ -510,6 +511,7 @@ __global__ void __launch_bounds__(PackedCfg<TN, C>::THREADS, 1)
       }
   }
   __syncthreads();
+  report_gave_up(*abort_flag);
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, Cfg::TMEM_COLS);
