@@ -375,7 +375,12 @@ def _launch(name: str, device: torch.device, stream, *args):
     device's current stream)."""
     if device.index != torch.cuda.current_device():
         with torch.cuda.device(device):
-            return _launch(name, device, stream, *args)
+            return _call(name, device, stream, *args)
+    _call(name, device, stream, *args)
+
+
+def _call(name: str, device: torch.device, stream, *args):
+    """_launch where `device` is current already."""
     rc = getattr(_lib or lib(), name)(
         *args, _raw_stream(device.index) if stream is None else stream.cuda_stream)
     if rc != OK:
@@ -574,6 +579,9 @@ def mx_linear(x: torch.Tensor, w: MxTensor, dtype: torch.dtype | None = None,
     _check_mx_input(x, fmt, tensor_scale, "mx_linear")
     m, k = x.shape
     device = x.device
+    if device.index != torch.cuda.current_device():  # the workspace's size depends on the device
+        with torch.cuda.device(device):
+            return mx_linear(x, w, dtype, tensor_scale, out, stream)
     dtype = dtype or x.dtype
     _check_mx_weights(w, fmt, k, device, dtype, "mx_linear")
     n = w.codes.shape[0]
@@ -581,9 +589,9 @@ def mx_linear(x: torch.Tensor, w: MxTensor, dtype: torch.dtype | None = None,
     f = MX_FORMATS[fmt]
     need = (_lib or lib()).admmq_mx_linear_workspace_bytes(m, n, k, f)
     ws = _empty((need,), torch.uint8, device, stream) if need else None
-    _launch("admmq_mx_linear", device, stream, x.data_ptr(), DTYPES[x.dtype], m, _row_stride(x),
-            _ptr_or_null(tensor_scale), *w._ptrs(), n, k, f, out.data_ptr(), DTYPES[dtype],
-            _ptr_or_null(ws), need)
+    _call("admmq_mx_linear", device, stream, x.data_ptr(), DTYPES[x.dtype], m, _row_stride(x),
+          _ptr_or_null(tensor_scale), *w._ptrs(), n, k, f, out.data_ptr(), DTYPES[dtype],
+          _ptr_or_null(ws), need)
     return out
 
 
