@@ -49,8 +49,8 @@ __global__ void __launch_bounds__(kMxThreads)
   const int col_tiles = (k + TILE_K - 1) / TILE_K;
   const int here = min(TILES, col_tiles - span * TILES);
   const int last = rows - row_tile * 128 < 128 ? (int)(rows - row_tile * 128) : 128;
-  // bytes of blocks or rows that do not exist are zero
-  if (last < 128 || (k % TILE_K != 0 && here < TILES + 1))
+  // bytes of blocks or rows that do not exist are zero (blocks: in a row's last tile)
+  if (last < 128 || (k % TILE_K != 0 && span == spans - 1))
     for (int i = threadIdx.x; i < TILES * kScaleTile / 16; i += kMxThreads)
       reinterpret_cast<uint4*>(tile)[i] = make_uint4(0, 0, 0, 0);
   __syncthreads();
