@@ -24,8 +24,10 @@ namespace {
 // 24576 x 4096 85.5 / 89.0, 25600 x 5120 dequantised 60 / 64).
 // What bounds them: HBM for 16-bit to mxfp4 (24576 x 4096 in about 40 us, 6.2 TB/s)
 // and for dequantisation (25600 x 5120 nvfp4 to bf16 57 us, 5.9 TB/s of 6.5); for
-// nvfp4 the conversions to e2m1, a few lanes a clock and SM, which every element
-// takes twice (see quantize16): 2047 x 12288 in 23 us, HBM would need 10.
+// nvfp4 instructions: 21 an element, which is rounded twice (see quantize16), 64 %
+// of the issue slots and 52 % of the ALU (no other pipe above 31 %), the rest of
+// the slots lost to loads, results and the tile's barriers: 2047 x 12288 in 23 us,
+// HBM would need 10.
 constexpr int kMxThreads = 256;
 constexpr int kMxWarps = kMxThreads / 32;
 

@@ -1,9 +1,10 @@
 // packed_few.cuh -- product of a few tokens (at most 16, used up to 12) with
 // packed b-bit codes, on mma.sync.  What bounds it is reading the weights once
 // and turning each code into an operand: instruction issue (three or four a
-// code of a lane, 4096 -> 24576 at 4 bits 21 us for 1 token where HBM needs 8),
-// which up to 8 tokens share, and for small layers the chain launch - load -
-// decode - sum (1 token of 4096 -> 6144 at 3 bits: 7.6 us device time of 1.7).
+// code of a lane, 4096 -> 24576 at 4 bits 21 us for 1 token where HBM needs 8, 62 %
+// of the issue slots taken), which up to 8 tokens share, and for small layers the
+// chain launch - load - decode - sum (1 token of 4096 -> 6144 at 3 bits: 7.6 us
+// device time of 1.7, 43 % of the slots: warps wait for results, words and barriers).
 //
 // mma.m16n8k16 sums over k in an order that nothing depends on, so each of the
 // four lanes that share a weight row takes 32 consecutive codes of a

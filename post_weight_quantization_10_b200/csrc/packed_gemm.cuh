@@ -13,9 +13,10 @@
 //
 // What bounds it: at 33 tokens of 12288 -> 4096 (2 bits, 22.5 us; HBM needs 2.6) a
 // chunk's chain of waits, decoding, stores and MMAs times the chunks of a rank;
-// at 4096 tokens of 4096 -> 24576 (4 bits) the power limit: 790 us in a burst,
-// 890 sustained, 1.04 and 0.93 PFLOP/s, where a bf16 product of that size takes
-// 503 and 592.  On the way there: 39 ms on the CUDA cores, 2.9 ms with one warp
+// at 4096 tokens of 4096 -> 24576 (4 bits) the MMAs wait for decoders and
+// group sums, the tensor pipe is active half of the cycles, and the power limit
+// sets the clock (1.62 GHz): 790 us in a burst, 890 sustained, 1.04 and 0.93
+// PFLOP/s, where a bf16 product of that size takes 503 and 592.  On the way there: 39 ms on the CUDA cores, 2.9 ms with one warp
 // group for everything, 1.4 with no division in the single-thread loops, 1.08
 // with a converged MMA warp, 0.91 with the decoding shared by two CTAs.
 #pragma once
